@@ -456,6 +456,152 @@ BEAM_MOE_API beam_moe_status beam_moe_ep_release(const beam_moe_ep_handle* handl
                                                  void* peer_ws);
 
 /*
+ * The layer's parts as operators of their own, with gradients: token rows
+ * sorted by expert and back, and the product of each expert's rows with that
+ * expert's weights. They serve layers the fused block does not cover (experts
+ * with biases, other activations or types, dense projections) and training on
+ * the routes beam_moe_route or a routing replay gives. A layer is
+ *   permute -> linear (swiglu, W13) -> linear (W2) -> combine
+ * and its backward the four backward calls in reverse. The conventions at the
+ * top of this file hold; rows may be of any width unless stated.
+ */
+typedef enum beam_moe_dtype {
+  BEAM_MOE_BF16 = 0,
+  BEAM_MOE_FP16 = 1,
+  BEAM_MOE_FP32 = 2
+} beam_moe_dtype;
+
+/* Supported: width 1..65536, n_experts 1..512, top_k 1..32, T * top_k up to
+ * 2^30. */
+typedef struct beam_moe_rows_cfg {
+  int32_t width;     /* H: elements per token row                             */
+  int32_t n_experts; /* E                                                     */
+  int32_t top_k;     /* K: experts per token                                  */
+  int32_t dtype;     /* beam_moe_dtype of the token rows                      */
+} beam_moe_rows_cfg;
+
+/*
+ * Token rows sorted by expert. Assignment (t, k) goes to row
+ *   pos[t][k] = offsets[e] + number of assignments before (t, k), in (t, k)
+ *               order, whose id is e as well,  e = topk_ids[t][k],
+ * and xp[pos[t][k]] = x[t]. Rows of expert e are offsets[e] .. offsets[e+1]-1.
+ * An id outside [0, E) names no expert (an expert of another rank, a padded
+ * token): pos is -1 and there is no row; rows from offsets[E] on are left as
+ * they were. An expert may occur more than once in a token's ids.
+ *   x        [T][H], topk_ids [T][K] int32, device
+ *   xp       [T*K][H], pos [T][K] int32, offsets [E+1] int32, device (out)
+ *   ws       beam_moe_permute_workspace_size(cfg, T) bytes
+ * T = 0 writes offsets (zeros) and nothing else.
+ */
+BEAM_MOE_API beam_moe_status beam_moe_permute_workspace_size(const beam_moe_rows_cfg* cfg,
+                                                             int64_t T, size_t* bytes);
+BEAM_MOE_API beam_moe_status beam_moe_permute(const beam_moe_rows_cfg* cfg, int64_t T,
+                                              const void* x, const int32_t* topk_ids, void* xp,
+                                              int32_t* pos, int32_t* offsets, void* ws,
+                                              size_t ws_bytes, void* stream);
+
+/* dx[t] = sum_k dxp[pos[t][k]] over the slots with a row, k ascending, summed
+ * in FP32. dxp [rows][H], dx [T][H] (out), both of cfg->dtype; a pos outside
+ * [0, rows) has no row. */
+BEAM_MOE_API beam_moe_status beam_moe_permute_backward(const beam_moe_rows_cfg* cfg, int64_t T,
+                                                       int64_t rows, const void* dxp,
+                                                       const int32_t* pos, void* dx,
+                                                       void* stream);
+
+/*
+ * Rows back to their tokens: out[t] = sum_k w[t][k] y[pos[t][k]] over the
+ * slots with a row, k ascending, FP32 FMAs, rounded once; a token without rows
+ * gets zeros.
+ *   y    [rows][H] of y_dtype: cfg->dtype or FP32
+ *   pos  [T][K] int32 (a pos outside [0, rows) has no row)
+ *   w    [T][K] fp32, or NULL: every weight is 1
+ *   out  [T][H] of cfg->dtype (out)
+ */
+BEAM_MOE_API beam_moe_status beam_moe_combine(const beam_moe_rows_cfg* cfg, int64_t T,
+                                              int64_t rows, const void* y, int32_t y_dtype,
+                                              const int32_t* pos, const float* w, void* out,
+                                              void* stream);
+
+/*
+ * The combine's gradients: dy[pos[t][k]] = w[t][k] dout[t] and
+ * dw[t][k] = <dout[t], y[pos[t][k]]> (FP32 sum; 0 where there is no row).
+ *   dout [T][H] of cfg->dtype; y, pos, w as for beam_moe_combine
+ *   dy   [rows][H] of y_dtype (out), or NULL; rows that no slot names are left
+ *        as they were; no two slots may name the same row (permute's do not)
+ *   dw   [T][K] fp32 (out), or NULL; y may be NULL without it
+ */
+BEAM_MOE_API beam_moe_status beam_moe_combine_backward(const beam_moe_rows_cfg* cfg, int64_t T,
+                                                       int64_t rows, const void* dout,
+                                                       const void* y, int32_t y_dtype,
+                                                       const int32_t* pos, const float* w,
+                                                       void* dy, float* dw, void* stream);
+
+typedef enum beam_moe_act {
+  BEAM_MOE_ACT_NONE = 0,
+  BEAM_MOE_ACT_RELU = 1,
+  BEAM_MOE_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2))                    */
+  BEAM_MOE_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) */
+  BEAM_MOE_ACT_SILU = 4,      /* z / (1 + e^-z)                               */
+  BEAM_MOE_ACT_SWIGLU = 5     /* silu(gate) * up: Z is [gate | up]            */
+} beam_moe_act;
+
+/* Supported: n_in and n_out multiples of 8 up to 65536, n_experts 1..512,
+ * dtype bf16 or fp16, up to 2^30 rows. */
+typedef struct beam_moe_linear_cfg {
+  int32_t n_in;      /* width of X                                            */
+  int32_t n_out;     /* width of Y                                            */
+  int32_t n_experts; /* E; 1: a dense layer                                   */
+  int32_t act;       /* beam_moe_act                                          */
+  int32_t dtype;     /* beam_moe_dtype of x, w, z and the gradients           */
+  int32_t out_fp32;  /* 1: y and residual are fp32; 0: of dtype               */
+} beam_moe_linear_cfg;
+
+/*
+ * Rows offsets[e] .. offsets[e+1]-1 through expert e:
+ *   Z = X W_e^T + bias_e,  Y = act(Z) + residual.
+ * Tensor-core products with FP32 accumulation; bias, activation and residual
+ * are added in FP32 before the one rounding. N is n_out, 2 n_out for swiglu
+ * (weight rows 0..n_out-1 gate, n_out..2 n_out-1 up, as W13 of the block).
+ *   x        [rows][n_in], w [E][N][n_in], device
+ *   bias     [E][N] fp32, residual [rows][n_out], or NULL
+ *   offsets  [E+1] int32, device, ascending (beam_moe_permute's); NULL with
+ *            E = 1: all rows. Rows outside every expert's are left as they
+ *            were. What points outside [0, rows] is cut off there.
+ *   y        [rows][n_out] (out); z [rows][N] of dtype (out), or NULL: Z for
+ *            the backward call. y may be the residual's buffer.
+ *   ws       beam_moe_linear_workspace_size(cfg, rows, 0) bytes; its status
+ *            word reports through beam_moe_check
+ * rows = 0 is a no-op.
+ */
+BEAM_MOE_API beam_moe_status beam_moe_linear_workspace_size(const beam_moe_linear_cfg* cfg,
+                                                            int64_t rows, int32_t backward,
+                                                            size_t* bytes);
+BEAM_MOE_API beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int64_t rows,
+                                             const void* x, const void* w, const float* bias,
+                                             const void* residual, const int32_t* offsets,
+                                             void* y, void* z, void* ws, size_t ws_bytes,
+                                             void* stream);
+
+/*
+ * Gradients of beam_moe_linear (the residual's gradient is dY itself):
+ *   dZ = dY act'(Z), dX = dZ W_e, dW_e = dZ^T X and dbias_e = sum dZ over the
+ * rows of e (zero for an expert without rows). dZ is rounded to dtype once as
+ * the products' operand; dbias sums it unrounded in FP32.
+ *   dy       [rows][n_out] of dtype; x, w, offsets as above
+ *   z        [rows][N] of dtype, beam_moe_linear's; NULL only with act none
+ *   dx       [rows][n_in], dw [E][N][n_in] of dtype, dbias [E][N] fp32 (out);
+ *            any may be NULL, not all. x may be NULL without dw, w without dx.
+ *   ws       beam_moe_linear_workspace_size(cfg, rows, 1) bytes
+ * rows = 0 writes dw and dbias (zeros).
+ */
+BEAM_MOE_API beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg,
+                                                      int64_t rows, const void* dy,
+                                                      const void* x, const void* w, const void* z,
+                                                      const int32_t* offsets, void* dx, void* dw,
+                                                      float* dbias, void* ws, size_t ws_bytes,
+                                                      void* stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word in the
  * workspace. *device_flags (may be NULL) receives the raw bits: 0x1 producer,
  * 0x2 MMA issuer, 0x4 epilogue gave up a bounded wait; 0x100 an expert id

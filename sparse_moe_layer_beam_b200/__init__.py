@@ -9,7 +9,10 @@ raises ImportError.
 The entry points mirror include/beam_moe.h one to one:
 beam_moe_workspace_size, beam_moe_route, beam_moe_forward,
 beam_moe_forward_routed, beam_moe_forward_traced, beam_moe_check, and the
-Trace wrapper of beam_moe_trace_*.
+Trace wrapper of beam_moe_trace_*. The row and linear operators
+(beam_moe_permute, beam_moe_combine, beam_moe_linear and their backward calls)
+check their tensors' types, shapes, strides and device here as well, since the
+library sees addresses only, and raise ValueError.
 """
 import ctypes
 import os
@@ -26,6 +29,10 @@ __all__ = ["BeamMoeCfg", "BeamMoeError", "Trace", "OP_ROUTE", "OP_FORWARD", "N_S
            "beam_moe_forward_stages", "beam_moe_workspace_layout", "BeamMoeWsLayout",
            "BeamMoeEpHandle", "beam_moe_ep_export", "beam_moe_ep_import",
            "beam_moe_ep_release", "EpPeers", "torch_gather",
+           "BeamMoeRowsCfg", "rows_cfg", "beam_moe_permute_workspace_size", "beam_moe_permute",
+           "beam_moe_permute_backward", "beam_moe_combine", "beam_moe_combine_backward",
+           "BeamMoeLinearCfg", "linear_cfg", "beam_moe_linear_workspace_size", "beam_moe_linear",
+           "beam_moe_linear_backward", "BF16", "FP16", "FP32", "ACTS",
            "beam_moe_check"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +44,8 @@ OP_FORWARD_NVFP4 = 2
 OP_FORWARD_HOST = 3
 OP_FORWARD_NVFP4_HOST = 4
 HOST_CHUNK = 8192
+BF16, FP16, FP32 = 0, 1, 2
+ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu", "swiglu")
 N_STAGES = 7
 STAGE_NAMES = ("router_gemm", "router_topk", "scan", "permute", "gateup_gemm", "down_gemm",
                "combine")
@@ -79,6 +88,19 @@ class BeamMoeEpHandle(ctypes.Structure):
                 ("bytes", ctypes.c_int64), ("device", ctypes.c_int32), ("pid", ctypes.c_int32)]
 
 
+class BeamMoeRowsCfg(ctypes.Structure):
+    """Token rows of the permute and combine operators."""
+    _fields_ = [("width", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class BeamMoeLinearCfg(ctypes.Structure):
+    """The linear operator: sizes, activation and types."""
+    _fields_ = [("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_fp32", ctypes.c_int32)]
+
+
 class BeamMoeError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -90,6 +112,8 @@ _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(BeamMoeCfg)
 _EP = ctypes.POINTER(BeamMoeEpCfg)
 _PP = ctypes.POINTER(ctypes.c_void_p)
+_ROWS = ctypes.POINTER(BeamMoeRowsCfg)
+_LIN = ctypes.POINTER(BeamMoeLinearCfg)
 _SIGS = {
     "beam_moe_workspace_size": [_CFG, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
     "beam_moe_route": [_CFG, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
@@ -126,6 +150,19 @@ _SIGS = {
     "beam_moe_ep_import": [ctypes.POINTER(BeamMoeEpHandle), ctypes.c_size_t,
                            ctypes.POINTER(ctypes.c_void_p)],
     "beam_moe_ep_release": [ctypes.POINTER(BeamMoeEpHandle), _P],
+    "beam_moe_permute_workspace_size": [_ROWS, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)],
+    "beam_moe_permute": [_ROWS, ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "beam_moe_permute_backward": [_ROWS, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P],
+    "beam_moe_combine": [_ROWS, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int32, _P, _P, _P,
+                         _P],
+    "beam_moe_combine_backward": [_ROWS, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int32,
+                                  _P, _P, _P, _P, _P],
+    "beam_moe_linear_workspace_size": [_LIN, ctypes.c_int64, ctypes.c_int32,
+                                       ctypes.POINTER(ctypes.c_size_t)],
+    "beam_moe_linear": [_LIN, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                        _P],
+    "beam_moe_linear_backward": [_LIN, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                 ctypes.c_size_t, _P],
     "beam_moe_trace_create": [ctypes.c_int32, ctypes.POINTER(_P)],
     "beam_moe_trace_destroy": [_P],
     "beam_moe_trace_reset": [_P],
@@ -340,6 +377,180 @@ class Trace:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------ row and linear operators
+
+_NAMES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
+_types = None
+
+
+def _torch_types():
+    """Tensor types accepted for each dtype (bf16 also as its 16-bit pattern)."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ((torch.bfloat16, torch.int16, torch.uint16), (torch.float16,),
+                  (torch.float32,), (torch.int32,))
+    return _types
+
+
+_I32 = 3
+
+
+def _tensor(name, t, kind, *shape):
+    """Address of a contiguous tensor of this type and shape on the current
+    CUDA device; None passes."""
+    if t is None:
+        return None
+    if t.dtype not in (_types or _torch_types())[kind]:
+        raise ValueError(f"{name}: unexpected type {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return _on_device(name, t)
+
+
+def _on_device(name, t):
+    d = t.get_device()
+    if d < 0 or d != _current_device():
+        raise ValueError(f"{name}: not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _need(name, t):
+    if t is None:
+        raise ValueError(f"{name}: a tensor is required")
+    return t
+
+
+def _bytes(ws):
+    """(address, bytes) of a workspace."""
+    return _on_device("ws", _need("ws", ws)), ws.numel() * ws.element_size()
+
+
+def rows_cfg(width, n_experts, top_k, dtype="bf16"):
+    """Token rows of `width` elements of dtype ("bf16", "fp16", "fp32"), routed
+    to top_k of n_experts."""
+    return BeamMoeRowsCfg(width, n_experts, top_k, _NAMES[dtype])
+
+
+def beam_moe_permute_workspace_size(cfg, T):
+    n = ctypes.c_size_t(0)
+    _check(lib().beam_moe_permute_workspace_size(ctypes.byref(cfg), T, ctypes.byref(n)),
+           "beam_moe_permute_workspace_size")
+    return n.value
+
+
+def beam_moe_permute(cfg, x, topk_ids, xp, pos, offsets, ws, stream=None):
+    """Token rows sorted by expert: x [T, H], topk_ids [T, K] int32 -> xp
+    [T*K, H], pos [T, K] int32, offsets [E+1] int32."""
+    T, K = _need("x", x).shape[0], cfg.top_k
+    d = cfg.dtype
+    args = (_tensor("x", x, d, T, cfg.width),
+            _tensor("topk_ids", _need("topk_ids", topk_ids), _I32, T, K),
+            _tensor("xp", _need("xp", xp), d, T * K, cfg.width),
+            _tensor("pos", _need("pos", pos), _I32, T, K),
+            _tensor("offsets", _need("offsets", offsets), _I32, cfg.n_experts + 1))
+    _check(lib().beam_moe_permute(ctypes.byref(cfg), T, *args, *_bytes(ws), _stream(stream)),
+           "beam_moe_permute")
+
+
+def beam_moe_permute_backward(cfg, dxp, pos, dx, stream=None):
+    """dx[t] = sum_k dxp[pos[t, k]]: dxp [rows, H], pos [T, K] -> dx [T, H]."""
+    T, rows = _need("dx", dx).shape[0], _need("dxp", dxp).shape[0]
+    args = (_tensor("dxp", dxp, cfg.dtype, rows, cfg.width),
+            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
+            _tensor("dx", dx, cfg.dtype, T, cfg.width))
+    _check(lib().beam_moe_permute_backward(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
+           "beam_moe_permute_backward")
+
+
+def _y_kind(cfg, y):
+    """FP32 for fp32 rows, else the configuration's dtype."""
+    return FP32 if y.dtype == (_types or _torch_types())[FP32][0] else cfg.dtype
+
+
+def beam_moe_combine(cfg, y, pos, w, out, stream=None):
+    """out[t] = sum_k w[t, k] y[pos[t, k]]: y [rows, H] of cfg's dtype or fp32,
+    w [T, K] fp32 or None (ones) -> out [T, H]."""
+    T, rows = _need("out", out).shape[0], _need("y", y).shape[0]
+    kind = _y_kind(cfg, y)
+    args = (_tensor("y", y, kind, rows, cfg.width), kind,
+            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
+            _tensor("w", w, FP32, T, cfg.top_k), _tensor("out", out, cfg.dtype, T, cfg.width))
+    _check(lib().beam_moe_combine(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
+           "beam_moe_combine")
+
+
+def beam_moe_combine_backward(cfg, dout, y, pos, w, dy, dw, stream=None):
+    """dy[pos[t, k]] = w[t, k] dout[t] (dy as y, or None), dw[t, k] =
+    <dout[t], y[pos[t, k]]> (fp32 [T, K], or None; y may be None without it)."""
+    T = _need("dout", dout).shape[0]
+    like = y if y is not None else _need("dy", dy)
+    rows, kind = like.shape[0], _y_kind(cfg, like)
+    args = (_tensor("dout", dout, cfg.dtype, T, cfg.width),
+            _tensor("y", y, kind, rows, cfg.width), kind,
+            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
+            _tensor("w", w, FP32, T, cfg.top_k), _tensor("dy", dy, kind, rows, cfg.width),
+            _tensor("dw", dw, FP32, T, cfg.top_k))
+    _check(lib().beam_moe_combine_backward(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
+           "beam_moe_combine_backward")
+
+
+def linear_cfg(n_in, n_out, n_experts=1, act="none", dtype="bf16", out_fp32=False):
+    """Y = act(X W^T + bias) + residual over n_experts' rows; act is one of
+    ACTS, dtype "bf16" or "fp16" (y and residual fp32 with out_fp32)."""
+    return BeamMoeLinearCfg(n_in, n_out, n_experts, ACTS.index(act), _NAMES[dtype],
+                            1 if out_fp32 else 0)
+
+
+def _weight_rows(cfg):
+    return cfg.n_out * 2 if ACTS[cfg.act] == "swiglu" else cfg.n_out
+
+
+def beam_moe_linear_workspace_size(cfg, rows, backward=False):
+    n = ctypes.c_size_t(0)
+    _check(lib().beam_moe_linear_workspace_size(ctypes.byref(cfg), rows, 1 if backward else 0,
+                                                ctypes.byref(n)),
+           "beam_moe_linear_workspace_size")
+    return n.value
+
+
+def beam_moe_linear(cfg, x, w, y, ws, bias=None, residual=None, offsets=None, z=None,
+                    stream=None):
+    """y = act(x w_e^T + bias_e) + residual for the rows of every expert e: x
+    [rows, n_in], w [E, N, n_in] (N = n_out, 2 n_out for swiglu), bias [E, N]
+    fp32, residual [rows, n_out], offsets [E+1] int32 (None: one expert) -> y
+    [rows, n_out] and, if given, z [rows, N] = x w_e^T + bias_e."""
+    rows, E, N, d = _need("x", x).shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
+    out = FP32 if cfg.out_fp32 else d
+    args = (_tensor("x", x, d, rows, cfg.n_in), _tensor("w", _need("w", w), d, E, N, cfg.n_in),
+            _tensor("bias", bias, FP32, E, N),
+            _tensor("residual", residual, out, rows, cfg.n_out),
+            _tensor("offsets", offsets, _I32, E + 1),
+            _tensor("y", _need("y", y), out, rows, cfg.n_out), _tensor("z", z, d, rows, N))
+    _check(lib().beam_moe_linear(ctypes.byref(cfg), rows, *args, *_bytes(ws), _stream(stream)),
+           "beam_moe_linear")
+
+
+def beam_moe_linear_backward(cfg, dy, x, w, ws, dx=None, dw=None, dbias=None, z=None,
+                             offsets=None, stream=None):
+    """Gradients of beam_moe_linear: dy [rows, n_out], x, w and the forward's z
+    -> dx [rows, n_in], dw [E, N, n_in], dbias [E, N] fp32 (each may be None)."""
+    rows, E, N, d = _need("dy", dy).shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
+    args = (_tensor("dy", dy, d, rows, cfg.n_out), _tensor("x", x, d, rows, cfg.n_in),
+            _tensor("w", w, d, E, N, cfg.n_in), _tensor("z", z, d, rows, N),
+            _tensor("offsets", offsets, _I32, E + 1), _tensor("dx", dx, d, rows, cfg.n_in),
+            _tensor("dw", dw, d, E, N, cfg.n_in), _tensor("dbias", dbias, FP32, E, N))
+    _check(lib().beam_moe_linear_backward(ctypes.byref(cfg), rows, *args, *_bytes(ws),
+                                          _stream(stream)), "beam_moe_linear_backward")
 
 
 # ------------------------------------------------------------ expert parallelism

@@ -1,0 +1,988 @@
+// linear.cu - products of expert-sorted rows with each expert's weights, on
+// 5th-generation tensor cores, and their gradients. Rows offsets[e] ..
+// offsets[e+1] - 1 belong to expert e (no offsets: one expert has all rows).
+//
+//   forward   Z = X W_e^T + b_e,  Y = act(Z) + residual       (contraction: in)
+//   backward  dZ = dY act'(Z)                                 (elementwise)
+//             dX = dZ W_e                                     (contraction: out)
+//             dW_e = sum over e's rows of dZ^T X              (contraction: rows)
+//             db_e = sum over e's rows of dZ
+//
+// One kernel does the three products (FWD, DGRAD, WGRAD). A tile is 128 rows
+// of D (X rows, or rows of dW_e) times BN columns. None of the operands is
+// transposed in memory: W_e in DGRAD and both operands in WGRAD are read by
+// TMA as they lie and declared MN-major to the MMA (their contraction runs
+// over shared-memory rows instead of columns).
+//
+//  - Rows of X or dZ beyond the segment of e inside a tile only fill lanes of
+//    the accumulator that are not stored. In WGRAD they would be summed, so
+//    the last step of a segment zeroes them in shared memory (both operands:
+//    0 times a NaN of another expert's row is a NaN) before its MMAs.
+//  - Contraction tails (in or out not a multiple of 64) are TMA's zero fill;
+//    W is a 3-D map, so that the fill starts at the end of each expert.
+//  - Enough tiles for the SMs: persistent CTAs, TMA producer, MMA issuer and
+//    four epilogue warps, accumulators double-buffered in TMEM. Fewer: a
+//    cluster of up to 8 CTAs splits the contraction of a tile and joins its
+//    partial sums through distributed shared memory, in CTA order.
+// Every wait is bounded (see sm100.cuh).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <string.h>
+
+#include "internal.h"
+#include "ops.h"
+#include "sm100.cuh"
+
+namespace beam {
+namespace {
+
+enum Mode { kFwd, kDgrad, kWgrad };
+
+constexpr int kThreads = 192;
+constexpr int kMaxE = 512;
+constexpr int kM = 128;       // rows of D per tile
+constexpr int kK = 64;        // contraction per pipeline stage
+constexpr int kRowGroup = 16; // row blocks that share a sweep over the columns
+constexpr int kBox = 64 * kK * 2;  // bytes of a 64 x 64 box
+
+struct LinParams {
+  const int32_t* offsets;  // [E + 1] or NULL
+  int E, rows;
+  int n_in, n_out, n_w;    // n_w: weight rows per expert (2 n_out for swiglu)
+  int cols;                // columns of D that exist (FWD n_out, else n_in)
+  int nk;                  // contraction steps (FWD, DGRAD)
+  int n_blk, m_blk;        // column tiles; row tiles of dW_e (WGRAD)
+  int box_a;               // rows per box of the row operand (FWD, DGRAD)
+  int act, fp16, out32;
+  const float* bias;       // [E][n_w] or NULL
+  const void* residual;    // [rows][n_out] or NULL
+  void* z;                 // [rows][n_w] or NULL
+  void* out;
+  unsigned* status;
+};
+
+template <int BN, bool SPLIT>
+struct LinCfg {
+  static constexpr int kABytes = kM * kK * 2;
+  static constexpr int kBBytes = BN * kK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  // persistent: all of shared memory; split: two CTAs per SM
+  static constexpr int kStages = SPLIT ? 4 : (192 * 1024) / kStageBytes;
+  static constexpr int kAccStages = SPLIT ? 1 : 2;
+  static constexpr int kTmemCols = kAccStages * BN;  // 64, 256 or 512
+  static constexpr int kBarBytes = 256;
+  static constexpr int kTabBytes = 4 * (3 * kMaxE + 16);
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kTabBytes;
+  static_assert(kSmemBytes <= 232448, "dynamic shared memory above the sm_100 limit");
+  static_assert(!SPLIT || kStages * kStageBytes >= kM * BN * 4, "partial tile in the ring");
+};
+
+// ------------------------------------------------------------- the segments
+// Segment of expert e, clamped into the rows there are whatever offsets holds.
+__device__ __forceinline__ void segment(const LinParams& p, int e, int& lo, int& cnt) {
+  if (!p.offsets) {
+    lo = 0;
+    cnt = p.rows;
+    return;
+  }
+  lo = min(max(__ldg(p.offsets + e), 0), p.rows);
+  cnt = min(max(__ldg(p.offsets + e + 1), lo), p.rows) - lo;
+}
+
+// In shared memory: first row and row count of every expert, and the prefix
+// of its 128-row blocks (rb[E]: all of them). THREADS threads call it.
+struct Segments {
+  int* lo;
+  int* cnt;
+  int* rb;
+};
+
+template <int THREADS>
+__device__ __forceinline__ void build_segments(const LinParams& p, const Segments& s, int* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = (kMaxE + THREADS - 1) / THREADS;
+  int blocks[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    blocks[i] = 0;
+    if (e < p.E) {
+      int lo, cnt;
+      segment(p, e, lo, cnt);
+      s.lo[e] = lo;
+      s.cnt[e] = cnt;
+      blocks[i] = (cnt + kM - 1) / kM;
+    }
+    sum += blocks[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  int run = inc - sum;
+  for (int w = 0; w < warp; ++w) run += scratch[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    if (e < p.E) {
+      s.rb[e] = run;
+      run += blocks[i];
+      if (e == p.E - 1) s.rb[p.E] = run;
+    }
+  }
+  __syncthreads();
+}
+
+// The expert whose row blocks hold block q (rb[0] <= q < rb[E]).
+__device__ __forceinline__ int find_expert(const int* rb, int E, int q) {
+  int a = 0, b = E;  // rb[a] <= q < rb[b]
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (rb[m] <= q) a = m;
+    else b = m;
+  }
+  return a;
+}
+
+struct Tile {
+  int e;
+  int row0;   // first row of D: a row of X / dX, or of dW_e
+  int rows;   // rows of the tile that exist
+  int n0;     // first column
+  int k0;     // WGRAD: first row of the segment
+  int kcnt;   // WGRAD: rows of the segment
+  int nk;     // contraction steps
+  bool once;  // the weight tile is read by this tile alone
+};
+
+// FWD and DGRAD: an expert's tiles go in groups of 16 row blocks, column tile
+// by column tile inside a group, row blocks fastest: the CTAs at work at one
+// time share a few weight tiles and at most 16 row blocks through L2.
+// WGRAD: row tiles of dW_e fastest in groups of 16 likewise.
+template <int MODE, int BN>
+__device__ __forceinline__ Tile decode(int t, const LinParams& p, const Segments& s, int bn_out) {
+  Tile d;
+  int e, m_blks, local;
+  if (MODE == kWgrad) {
+    const int per = p.m_blk * p.n_blk;
+    e = t / per;
+    local = t - e * per;
+    m_blks = p.m_blk;
+  } else {
+    e = find_expert(s.rb, p.E, t / p.n_blk);
+    local = t - s.rb[e] * p.n_blk;
+    m_blks = s.rb[e + 1] - s.rb[e];
+  }
+  const int g = local / (kRowGroup * p.n_blk);
+  const int in_g = min(kRowGroup, m_blks - g * kRowGroup);
+  const int rem = local - g * kRowGroup * p.n_blk;
+  const int nb = rem / in_g;
+  const int mb = g * kRowGroup + rem - nb * in_g;
+  d.e = e;
+  d.n0 = nb * bn_out;
+  d.once = m_blks == 1;
+  if (MODE == kWgrad) {
+    segment(p, e, d.k0, d.kcnt);
+    d.nk = (d.kcnt + kK - 1) / kK;
+    d.row0 = mb * kM;
+    d.rows = min(kM, p.n_w - d.row0);
+  } else {
+    d.k0 = 0;
+    d.kcnt = 0;
+    d.nk = p.nk;
+    d.row0 = s.lo[e] + mb * kM;
+    d.rows = min(kM, s.cnt[e] - mb * kM);
+  }
+  return d;
+}
+
+// -------------------------------------------------------------- descriptors
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+      "l"(policy)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: boxes of 64 (contraction) rows x 64
+// elements, 8 KB apart (leading offset), rows in groups of 8 that lie 1 KB
+// apart (stride offset). 16 contraction rows further: 2 KB.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kBox >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+template <int MODE>
+__device__ __forceinline__ uint32_t idesc_of(bool fp16, uint32_t N) {
+  const uint32_t fmt = fp16 ? 0u : 1u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((MODE == kWgrad ? 1u : 0u) << 15) |
+         ((MODE != kFwd ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// ----------------------------------------------------------------- epilogue
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// 1/2 (1 + erf(z / sqrt 2)) as a complement: relative accuracy down the tail.
+__device__ __forceinline__ float normal_cdf(float z) {
+  return 0.5f * erfcf(z * -0.70710678118654752f);
+}
+
+// 1/2 (1 + tanh(a)) = sigmoid(2 a) for a = sqrt(2/pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float tanh_gate(float z) {
+  return sigmoid_f(1.59576912160573071f * fmaf(0.044715f * z * z, z, z));
+}
+
+__device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    case BEAM_MOE_ACT_RELU: return z > 0.0f ? z : 0.0f;
+    case BEAM_MOE_ACT_GELU: return z * normal_cdf(z);
+    case BEAM_MOE_ACT_GELU_TANH: return z * tanh_gate(z);
+    case BEAM_MOE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t v, bool fp16) {
+  return fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+              : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// 4 consecutive elements at p (element index at, a multiple of 4).
+__device__ __forceinline__ void store4(void* p, int64_t at, const float* v, bool f32, bool fp16) {
+  if (f32)
+    reinterpret_cast<float4*>(static_cast<float*>(p) + at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at)[0] =
+        make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
+}
+
+__device__ __forceinline__ void load4(const void* p, int64_t at, float* v, bool f32, bool fp16) {
+  if (f32) {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    const float2 a = unpack16(u.x, fp16), b = unpack16(u.y, fp16);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+}
+
+// Four columns n .. n + 3 of one row of D: a (and, for swiglu, the up values
+// u). n_out and n_in are multiples of 8, so four columns exist together.
+template <int MODE>
+__device__ __forceinline__ void finish4(const LinParams& p, const Tile& t, int r, int n, float* a,
+                                        float* u) {
+  if (n >= p.cols) return;
+  if (MODE == kWgrad) {
+    store4(p.out, ((int64_t)t.e * p.n_w + t.row0 + r) * p.n_in + n, a, false, p.fp16);
+    return;
+  }
+  const int64_t row = t.row0 + r;
+  if (MODE == kDgrad) {
+    store4(p.out, row * p.n_in + n, a, false, p.fp16);
+    return;
+  }
+  const bool glu = p.act == BEAM_MOE_ACT_SWIGLU;
+  if (p.bias) {
+    const float* b = p.bias + (int64_t)t.e * p.n_w + n;
+    const float4 f = __ldg(reinterpret_cast<const float4*>(b));
+    a[0] += f.x; a[1] += f.y; a[2] += f.z; a[3] += f.w;
+    if (glu) {
+      const float4 g = __ldg(reinterpret_cast<const float4*>(b + p.n_out));
+      u[0] += g.x; u[1] += g.y; u[2] += g.z; u[3] += g.w;
+    }
+  }
+  if (p.z) {
+    store4(p.z, row * p.n_w + n, a, false, p.fp16);
+    if (glu) store4(p.z, row * p.n_w + p.n_out + n, u, false, p.fp16);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    a[j] = glu ? activate(BEAM_MOE_ACT_SILU, a[j]) * u[j] : activate(p.act, a[j]);
+  if (p.residual) {
+    float q[4];
+    load4(p.residual, row * p.n_out + n, q, p.out32, p.fp16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] += q[j];
+  }
+  store4(p.out, row * p.n_out + n, a, p.out32, p.fp16);
+}
+
+// ------------------------------------------------------------------- kernel
+template <int MODE, int BN, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const LinParams p) {
+  using C = LinCfg<BN, SPLIT>;
+  constexpr int STAGES = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* tab = reinterpret_cast<int*>(smem + STAGES * C::kStageBytes + C::kBarBytes);
+  const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
+  int* scratch = tab + 3 * kMaxE + 1;  // a word per warp
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
+  uint32_t parts = 1;
+  if (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 128);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_holder, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (MODE != kWgrad) build_segments<kThreads>(p, seg, scratch);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
+  const int bn_out = glu ? BN / 2 : BN;
+  const int total = MODE == kWgrad ? p.E * p.m_blk * p.n_blk : seg.rb[p.E] * p.n_blk;
+  const int first = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int step = SPLIT ? total : gridDim.x;  // split: one tile per cluster
+  // this CTA's contraction steps of a tile
+  auto k_range = [&](const Tile& t, int& ka, int& kb) {
+    ka = SPLIT ? (int)((int64_t)t.nk * rank / parts) : 0;
+    kb = SPLIT ? (int)((int64_t)t.nk * (rank + 1) / parts) : t.nk;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      const uint64_t pol_stream = policy_evict_first();
+      const uint64_t pol_keep = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int ti = first; ti < total && ok; ti += step) {
+        const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
+        int ka, kb;
+        k_range(t, ka, kb);
+        const int boxes_a = MODE == kWgrad ? 2 : (t.rows + p.box_a - 1) / p.box_a;
+        const uint32_t bytes_a = MODE == kWgrad ? C::kABytes : boxes_a * p.box_a * kK * 2;
+        const uint64_t pol_w = t.once ? pol_stream : pol_keep;
+        for (int k = ka; k < kb; ++k) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kFlagProducer)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * C::kStageBytes;
+          uint8_t* sb = sa + C::kABytes;
+          mbar_arrive_expect_tx(&full[stage], bytes_a + C::kBBytes);
+          if (MODE == kWgrad) {
+            const int r = t.k0 + k * kK;
+            for (int b = 0; b < 2; ++b)
+              tma_load_2d(sa + b * kBox, &tm_a, &full[stage], t.row0 + b * 64, r, pol_keep);
+#pragma unroll
+            for (int b = 0; b < BN / 64; ++b)
+              tma_load_2d(sb + b * kBox, &tm_b, &full[stage], t.n0 + b * 64, r, pol_keep);
+          } else {
+            for (int b = 0; b < boxes_a; ++b)
+              tma_load_2d(sa + b * p.box_a * kK * 2, &tm_a, &full[stage], k * kK,
+                          t.row0 + b * p.box_a, pol_keep);
+            if (MODE == kFwd) {
+              tma_load_3d(sb, &tm_b, &full[stage], k * kK, t.n0, t.e, pol_w);
+              if (glu)
+                tma_load_3d(sb + C::kBBytes / 2, &tm_b, &full[stage], k * kK, p.n_out + t.n0, t.e,
+                            pol_w);
+            } else {
+#pragma unroll
+              for (int b = 0; b < BN / 64; ++b)
+                tma_load_3d(sb + b * kBox, &tm_b, &full[stage], t.n0 + b * 64, k * kK, t.e, pol_w);
+            }
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Let every copy this thread issued land before the CTA can exit.
+      const int64_t from = issued > STAGES ? issued - STAGES : 0;
+      for (int64_t i = from; i < issued; ++i)
+        mbar_wait(&full[i % STAGES], (uint32_t)((i / STAGES) & 1), nullptr, nullptr, 0u,
+                  100000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    // The whole warp walks the tiles (it zeroes the rows behind a segment in
+    // WGRAD together); lane 0 issues.
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    const uint32_t idesc = idesc_of<MODE>(p.fp16, BN);
+    for (int ti = first; ti < total && ok; ti += step) {
+      const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
+      int ka, kb;
+      k_range(t, ka, kb);
+      if (ka == kb) continue;  // nothing to add: the epilogue takes zeros
+      if (!SPLIT) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status,
+                                               kFlagMma));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+      for (int k = ka; k < kb; ++k) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&full[stage], phase, abort_flag, p.status, kFlagMma));
+        if (!ok) break;
+        const uint32_t sa = smem_addr(smem + stage * C::kStageBytes);
+        const uint32_t sb = sa + C::kABytes;
+        int k16 = kK / 16;
+        if (MODE == kWgrad) {
+          const int rem = t.kcnt - k * kK;  // rows of the segment in this step
+          if (rem < kK) {
+            k16 = (rem + 15) / 16;
+            const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
+            uint4* base = reinterpret_cast<uint4*>(smem + stage * C::kStageBytes);
+            for (int i = lane; i < dirty * 8 * (2 + BN / 64); i += 32) {
+              const int box = i / (dirty * 8), j = i - box * dirty * 8;
+              base[box * (kBox / 16) + rem * 8 + j] = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t da = MODE == kWgrad ? smem_desc_mn_sw128(sa) : smem_desc_k_sw128(sa);
+          const uint64_t db = MODE == kFwd ? smem_desc_k_sw128(sb) : smem_desc_mn_sw128(sb);
+          constexpr uint32_t kStepA = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
+          constexpr uint32_t kStepB = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
+          for (int q = 0; q < k16; ++q)
+            umma_bf16(d, da + kStepA * q, db + kStepB * q, idesc, (k - ka) | q);
+          umma_commit(&empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(&tfull[acc]);
+      __syncwarp();
+      if (!SPLIT) {
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) {
+      // Every MMA this thread issued completes before TMEM is released.
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, nullptr, 0u, 100000000ull);
+    }
+    __syncwarp();
+  } else if (!SPLIT) {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    const int r = q * 32 + lane;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int ti = first; ti < total; ti += step) {
+      const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
+      const bool none = t.nk == 0;
+      if (!none) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status,
+                                               kFlagEpilogue)))
+          break;
+        tc_fence_after();
+      }
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+      for (int c0 = 0; c0 < bn_out && t.n0 + c0 < p.cols; c0 += 16) {
+        uint32_t a[16], u[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = u[j] = 0u;
+        if (!none) {
+          tmem_ld16(tb + c0, a);
+          if (glu) tmem_ld16(tb + BN / 2 + c0, u);
+          tmem_ld_wait();
+        }
+        if (r < t.rows) {
+          float* fa = reinterpret_cast<float*>(a);
+          float* fu = reinterpret_cast<float*>(u);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) finish4<MODE>(p, t, r, t.n0 + c0 + j, fa + j, fu + j);
+        }
+      }
+      if (!none) {
+        tc_fence_before();
+        mbar_arrive(&tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+
+  if (SPLIT) {
+    // Each CTA leaves its partial sums in its own shared memory, column by
+    // column (the ring is free: its MMAs are done), and finishes bn_out/parts
+    // columns, adding the parts in CTA order.
+    const int q = warp & 3, r = q * 32 + lane;
+    float* part = reinterpret_cast<float*>(smem);
+    const bool have = first < total;
+    Tile t;
+    if (have) t = decode<MODE, BN>(first, p, seg, bn_out);
+    if (warp >= 2 && have) {
+      int ka, kb;
+      k_range(t, ka, kb);
+      const bool got = ka < kb && __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, abort_flag,
+                                                                   p.status, kFlagEpilogue));
+      tc_fence_after();
+      for (int c0 = 0; c0 < BN; c0 += 16) {
+        uint32_t a[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = 0u;
+        if (got) {
+          tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c0, a);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c0 + j) * kM + r] = __uint_as_float(a[j]);
+      }
+    }
+    cluster_sync();
+    if (warp >= 2 && have && r < t.rows) {
+      const int per = bn_out / (int)parts;  // 4 at least
+      const uint32_t mine = smem_addr(part) + 4u * r;
+      for (int c0 = rank * per; c0 < (int)(rank + 1) * per; c0 += 4) {
+        float a[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t s = 0; s < parts; ++s) {
+          const uint32_t from = mapa_shared(mine, s);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] += ld_dsmem_f32(from + 4u * kM * (c0 + j));
+            if (glu) u[j] += ld_dsmem_f32(from + 4u * kM * (BN / 2 + c0 + j));
+          }
+        }
+        finish4<MODE>(p, t, r, t.n0 + c0, a, u);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its part
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// ----------------------------------------- dZ and the sums of dZ over rows
+constexpr int kActThreads = 256;
+constexpr int kActCols = 256;  // columns of Y per CTA: 32 threads of 8; 8 rows at a time
+
+// act'(z) dy in FP32.
+__device__ __forceinline__ float act_grad(int act, float dy, float z) {
+  switch (act) {
+    case BEAM_MOE_ACT_RELU: return z > 0.0f ? dy : 0.0f;
+    case BEAM_MOE_ACT_GELU: {
+      return dy * fmaf(z, 0.39894228040143268f * __expf(-0.5f * z * z), normal_cdf(z));
+    }
+    case BEAM_MOE_ACT_GELU_TANH: {
+      const float s = tanh_gate(z);  // its slope is s (1 - s) 2 da/dz
+      return dy * fmaf(z * s * (1.0f - s),
+                       1.59576912160573071f * fmaf(3.0f * 0.044715f, z * z, 1.0f), s);
+    }
+    case BEAM_MOE_ACT_SILU: {
+      const float s = sigmoid_f(z);
+      return dy * s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    default: return dy;
+  }
+}
+
+struct ActParams {
+  const uint16_t* dy;
+  const uint16_t* z;  // NULL: act none
+  uint16_t* dz;       // NULL: act none
+  float* part;        // [row blocks][n_w] or NULL
+};
+
+// One 128-row block of one expert x 256 columns: dZ (rounded to 16 bits, the
+// products' operand type) and the block's column sums of the unrounded dZ.
+// Bound by HBM: dY and Z in, dZ out.
+__global__ void __launch_bounds__(kActThreads)
+    act_backward_kernel(const LinParams p, const ActParams a) {
+  __shared__ int tab[3 * kMaxE + 1 + 8];
+  __shared__ float s_sum[8][2][kActCols + 8];
+  const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
+  build_segments<kActThreads>(p, seg, tab + 3 * kMaxE + 1);
+  const int q = blockIdx.x;
+  if (q >= seg.rb[p.E]) return;
+  const int e = find_expert(seg.rb, p.E, q);
+  const int i0 = (q - seg.rb[e]) * kM;
+  const int64_t row0 = seg.lo[e] + i0;
+  const int nrows = min(kM, seg.cnt[e] - i0);
+  const bool glu = p.act == BEAM_MOE_ACT_SWIGLU, fp16 = p.fp16;
+  const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int n = blockIdx.y * kActCols + cl * 8;
+  float sum[8], sumu[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = sumu[j] = 0.0f;
+  if (n < p.n_out) {
+#pragma unroll 4
+    for (int r = rl; r < nrows; r += 8) {
+      float g[8], z[8], u[8];
+      load4(a.dy, (row0 + r) * p.n_out + n, g, false, fp16);
+      load4(a.dy, (row0 + r) * p.n_out + n + 4, g + 4, false, fp16);
+      if (a.z) {
+        const int64_t at = (row0 + r) * p.n_w + n;
+        load4(a.z, at, z, false, fp16);
+        load4(a.z, at + 4, z + 4, false, fp16);
+        if (glu) {
+          load4(a.z, at + p.n_out, u, false, fp16);
+          load4(a.z, at + p.n_out + 4, u + 4, false, fp16);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (glu) {
+            const float s = sigmoid_f(z[j]), d = g[j];
+            g[j] = d * u[j] * s * fmaf(z[j], 1.0f - s, 1.0f);
+            u[j] = d * z[j] * s;
+            sumu[j] += u[j];
+          } else {
+            g[j] = act_grad(p.act, g[j], z[j]);
+          }
+        }
+        store4(a.dz, at, g, false, fp16);
+        store4(a.dz, at + 4, g + 4, false, fp16);
+        if (glu) {
+          store4(a.dz, at + p.n_out, u, false, fp16);
+          store4(a.dz, at + p.n_out + 4, u + 4, false, fp16);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s_sum[rl][0][cl * 8 + j] = sum[j];
+    s_sum[rl][1][cl * 8 + j] = sumu[j];
+  }
+  __syncthreads();
+  const int c = blockIdx.y * kActCols + threadIdx.x;
+  if (c < p.n_out) {
+    for (int h = 0; h < (glu ? 2 : 1); ++h) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v += s_sum[w][h][threadIdx.x];
+      a.part[(int64_t)q * p.n_w + h * p.n_out + c] = v;
+    }
+  }
+}
+
+// dbias[e] = the sums of e's row blocks, 8 interleaved chains joined in order.
+__global__ void __launch_bounds__(kActThreads)
+    bias_join_kernel(const LinParams p, const float* __restrict__ part, float* __restrict__ dbias) {
+  __shared__ int tab[3 * kMaxE + 1 + 8];
+  __shared__ float s_sum[8][32];
+  const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
+  build_segments<kActThreads>(p, seg, tab + 3 * kMaxE + 1);
+  const int e = blockIdx.x;
+  const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int c = blockIdx.y * 32 + cl;
+  float v = 0.0f;
+  if (c < p.n_w)
+#pragma unroll 4
+    for (int q = seg.rb[e] + rl; q < seg.rb[e + 1]; q += 8) v += __ldg(part + (int64_t)q * p.n_w + c);
+  s_sum[rl][cl] = v;
+  __syncthreads();
+  if (rl == 0 && c < p.n_w) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s_sum[w][cl];
+    dbias[(int64_t)e * p.n_w + c] = t;
+  }
+}
+
+// ------------------------------------------------------------------- launches
+template <int MODE, int BN, bool SPLIT>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p,
+                         int64_t tiles, int parts, cudaStream_t st) {
+  using C = LinCfg<BN, SPLIT>;
+  static PerDevice configured;  // the shared-memory attribute, once per device
+  int unused = 0;
+  cudaError_t err = per_device(configured, &unused, [](int*) {
+    return cudaFuncSetAttribute(linear_kernel<MODE, BN, SPLIT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  });
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  const int64_t sms = device_sm_count();
+  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * parts : (tiles < sms ? tiles : sms)));
+  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BN, SPLIT>, ta, tb, p);
+}
+
+// The product of one mode. Column tiles of 256 while those make a tile for
+// every SM, else of 128, else of 64 with the contraction split over a cluster
+// (at least 4 steps a CTA).
+template <int MODE>
+cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
+  LinParams p = base;
+  const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
+  const int64_t R = p.rows, E = p.E;
+  const int64_t sms = device_sm_count();
+  // row blocks: at most this many (every expert may end inside one)
+  const int64_t rb = MODE == kWgrad ? E * ((p.n_w + kM - 1) / kM) : R / kM + (E < R ? E : R);
+  const int64_t rb_sure = MODE == kWgrad ? rb : (R + kM - 1) / kM > E / 2 ? (R + kM - 1) / kM
+                                                                          : (E < R ? E : R) / 2;
+  auto blocks = [&](int bn) { return (p.cols + (glu ? bn / 2 : bn) - 1) / (glu ? bn / 2 : bn); };
+  int bn = 64;
+  if (rb_sure * blocks(256) >= sms) bn = 256;
+  else if (rb_sure * blocks(128) >= sms) bn = 128;
+  p.n_blk = blocks(bn);
+  p.m_blk = (p.n_w + kM - 1) / kM;
+  const int kc = MODE == kFwd ? p.n_in : p.n_w;
+  p.nk = (kc + kK - 1) / kK;
+  const int64_t tiles = rb * p.n_blk;
+  const int64_t steps = MODE == kWgrad ? (R / E + kK - 1) / kK : p.nk;
+  int parts = 1;
+  while (bn == 64 && parts < 8 && rb_sure * p.n_blk * parts * 2 <= 2 * sms && steps >= 8 * parts)
+    parts *= 2;
+  // boxes of the row operand: about an expert's rows, so that few rows cost
+  // few bytes; 8 .. 128
+  p.box_a = 8;
+  while (p.box_a < 128 && p.box_a < 2 * R / E) p.box_a *= 2;
+
+  CUtensorMap ta, tb;
+  cudaError_t err;
+  if (MODE == kWgrad) {
+    err = encode_tmap_2d_bf16(&ta, a, p.n_w, R, 64, 64);
+    if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, b, p.n_in, R, 64, 64);
+  } else {
+    err = encode_tmap_2d_bf16(&ta, a, kc, R, 64, p.box_a);
+    if (err == cudaSuccess)
+      err = encode_tmap_3d_bf16(&tb, b, p.n_in, p.n_w, E, 64,
+                                MODE == kDgrad ? 64 : (glu ? bn / 2 : bn));
+  }
+  if (err != cudaSuccess) return err;
+  if (bn == 256) return launch_tiles<MODE, 256, false>(ta, tb, p, tiles, 1, st);
+  if (bn == 128) return launch_tiles<MODE, 128, false>(ta, tb, p, tiles, 1, st);
+  return launch_tiles<MODE, 64, true>(ta, tb, p, tiles, parts, st);
+}
+
+struct LinLayout {
+  size_t part, dz, total;
+  int64_t blocks;  // row blocks at most
+};
+
+int weight_rows(const beam_moe_linear_cfg& c) {
+  return c.act == BEAM_MOE_ACT_SWIGLU ? 2 * c.n_out : c.n_out;
+}
+
+LinLayout lin_layout(const beam_moe_linear_cfg& c, int64_t rows, bool backward) {
+  LinLayout L;
+  const int64_t E = c.n_experts;
+  L.blocks = rows / kM + (E < rows ? E : rows);
+  L.part = 256;
+  L.dz = L.part;
+  L.total = 256;
+  if (backward) {
+    const size_t n_w = (size_t)weight_rows(c);
+    L.dz = (L.part + (size_t)L.blocks * n_w * 4 + 1023) / 1024 * 1024;
+    L.total = L.dz + (c.act == BEAM_MOE_ACT_NONE ? 0 : ((size_t)rows * n_w * 2 + 255) / 256 * 256);
+  }
+  return L;
+}
+
+beam_moe_status check_linear(const beam_moe_linear_cfg* c, int64_t rows) {
+  if (!c || rows < 0) return BEAM_MOE_ERR_INVALID_ARG;
+  if (c->n_in <= 0 || c->n_out <= 0 || c->n_experts <= 0) return BEAM_MOE_ERR_INVALID_ARG;
+  if (c->act < BEAM_MOE_ACT_NONE || c->act > BEAM_MOE_ACT_SWIGLU) return BEAM_MOE_ERR_INVALID_ARG;
+  if (c->dtype != BEAM_MOE_BF16 && c->dtype != BEAM_MOE_FP16) return BEAM_MOE_ERR_INVALID_ARG;
+  if (c->out_fp32 != 0 && c->out_fp32 != 1) return BEAM_MOE_ERR_INVALID_ARG;
+  if (c->n_in % 8 || c->n_out % 8 || c->n_in > 65536 || c->n_out > 65536 || c->n_experts > kMaxE)
+    return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows > (int64_t)1 << 30) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
+  return BEAM_MOE_OK;
+}
+
+beam_moe_status check_linear_ws(const beam_moe_linear_cfg* c, int64_t rows, bool backward,
+                                const void* offsets, const void* ws, size_t ws_bytes) {
+  if (!ws || (c->n_experts > 1 && !offsets)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) & 15u) return BEAM_MOE_ERR_ALIGNMENT;
+  if (ws_bytes < lin_layout(*c, rows, backward).total) return BEAM_MOE_ERR_WORKSPACE_TOO_SMALL;
+  return BEAM_MOE_OK;
+}
+
+LinParams lin_params(const beam_moe_linear_cfg& c, int64_t rows, const int32_t* offsets, void* ws) {
+  LinParams p;
+  memset(&p, 0, sizeof(p));
+  p.offsets = offsets;
+  p.E = c.n_experts;
+  p.rows = (int)rows;
+  p.n_in = c.n_in;
+  p.n_out = c.n_out;
+  p.n_w = weight_rows(c);
+  p.act = c.act;
+  p.fp16 = c.dtype == BEAM_MOE_FP16;
+  p.out32 = c.out_fp32;
+  p.status = static_cast<unsigned*>(ws);
+  return p;
+}
+
+}  // namespace
+}  // namespace beam
+
+#define LIN_TRY(expr)                        \
+  do {                                       \
+    const beam_moe_status s_ = (expr);       \
+    if (s_ != BEAM_MOE_OK) return s_;        \
+  } while (0)
+
+#define LIN_CUDA(expr)                                          \
+  do {                                                          \
+    if ((expr) != cudaSuccess) return BEAM_MOE_ERR_CUDA;        \
+  } while (0)
+
+extern "C" {
+
+beam_moe_status beam_moe_linear_workspace_size(const beam_moe_linear_cfg* cfg, int64_t rows,
+                                               int32_t backward, size_t* bytes) {
+  LIN_TRY(beam::check_linear(cfg, rows));
+  if (!bytes || (backward != 0 && backward != 1)) return BEAM_MOE_ERR_INVALID_ARG;
+  *bytes = beam::lin_layout(*cfg, rows, backward == 1).total;
+  return BEAM_MOE_OK;
+}
+
+beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int64_t rows, const void* x,
+                                const void* w, const float* bias, const void* residual,
+                                const int32_t* offsets, void* y, void* z, void* ws,
+                                size_t ws_bytes, void* stream) {
+  LIN_TRY(beam::check_linear(cfg, rows));
+  if (rows == 0) return BEAM_MOE_OK;
+  LIN_TRY(beam::check_ops_ptrs({x, w, y}, {bias, residual, offsets, z}));
+  LIN_TRY(beam::check_linear_ws(cfg, rows, false, offsets, ws, ws_bytes));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  beam::LinParams p = beam::lin_params(*cfg, rows, offsets, ws);
+  p.cols = cfg->n_out;
+  p.bias = bias;
+  p.residual = residual;
+  p.z = z;
+  p.out = y;
+  LIN_CUDA(cudaMemsetAsync(ws, 0, 256, st));
+  LIN_CUDA(beam::launch_product<beam::kFwd>(p, x, w, st));
+  return BEAM_MOE_OK;
+}
+
+beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t rows,
+                                         const void* dy, const void* x, const void* w,
+                                         const void* z, const int32_t* offsets, void* dx, void* dw,
+                                         float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  LIN_TRY(beam::check_linear(cfg, rows));
+  if (!dx && !dw && !dbias) return BEAM_MOE_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t n_w = (size_t)beam::weight_rows(*cfg), E = (size_t)cfg->n_experts;
+  if (rows == 0) {  // no rows: the sums over rows are zero
+    LIN_TRY(beam::check_ops_ptrs({}, {dw, dbias}));
+    if (dw) LIN_CUDA(cudaMemsetAsync(dw, 0, E * n_w * cfg->n_in * 2, st));
+    if (dbias) LIN_CUDA(cudaMemsetAsync(dbias, 0, E * n_w * 4, st));
+    return BEAM_MOE_OK;
+  }
+  if ((dw && !x) || (dx && !w)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (cfg->act != BEAM_MOE_ACT_NONE && !z) return BEAM_MOE_ERR_INVALID_ARG;
+  LIN_TRY(beam::check_ops_ptrs({dy}, {x, w, z, offsets, dx, dw, dbias}));
+  LIN_TRY(beam::check_linear_ws(cfg, rows, true, offsets, ws, ws_bytes));
+  const beam::LinLayout L = beam::lin_layout(*cfg, rows, true);
+  char* base = static_cast<char*>(ws);
+  beam::LinParams p = beam::lin_params(*cfg, rows, offsets, ws);
+  const bool acted = cfg->act != BEAM_MOE_ACT_NONE;
+  const void* dz = acted ? static_cast<const void*>(base + L.dz) : dy;
+  LIN_CUDA(cudaMemsetAsync(ws, 0, 256, st));
+  if (acted || dbias) {
+    beam::ActParams a;
+    a.dy = static_cast<const uint16_t*>(dy);
+    a.z = acted ? static_cast<const uint16_t*>(z) : nullptr;
+    a.dz = acted ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
+    a.part = dbias ? reinterpret_cast<float*>(base + L.part) : nullptr;
+    const dim3 grid((unsigned)L.blocks,
+                    (unsigned)((cfg->n_out + beam::kActCols - 1) / beam::kActCols));
+    beam::act_backward_kernel<<<grid, beam::kActThreads, 0, st>>>(p, a);
+    LIN_CUDA(cudaGetLastError());
+    if (dbias) {
+      const dim3 jgrid((unsigned)E, (unsigned)((n_w + 31) / 32));
+      beam::bias_join_kernel<<<jgrid, beam::kActThreads, 0, st>>>(p, a.part, dbias);
+      LIN_CUDA(cudaGetLastError());
+    }
+  }
+  p.cols = cfg->n_in;
+  if (dx) {
+    p.out = dx;
+    LIN_CUDA(beam::launch_product<beam::kDgrad>(p, dz, w, st));
+  }
+  if (dw) {
+    p.out = dw;
+    LIN_CUDA(beam::launch_product<beam::kWgrad>(p, dz, x, st));
+  }
+  return BEAM_MOE_OK;
+}
+
+}  // extern "C"
