@@ -156,6 +156,22 @@ cudaError_t encode_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t col
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Weights [mats][2 n][k] (n gate rows, then n up rows) as 4-D {k, n, 2, mats}:
+// a box {64, 16, 2, 1} lands as 16 gate rows and the same 16 up rows.
+cudaError_t encode_tmap_glu_bf16(CUtensorMap* map, const void* base, uint64_t k, uint64_t n,
+                                 uint64_t mats) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {k, n, 2, mats};
+  const cuuint64_t strides[3] = {k * 2, n * k * 2, 2 * n * k * 2};
+  const cuuint32_t box[4] = {64, 16, 2, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // 2-D byte tensor [rows][cols], box {box_cols, box_rows}, 128-byte swizzle.
 cudaError_t encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                               uint32_t box_cols, uint32_t box_rows) {

@@ -204,6 +204,9 @@ cudaError_t encode_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t col
 cudaError_t encode_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                                 uint64_t mats, uint32_t box_cols, uint32_t box_rows);
 
+cudaError_t encode_tmap_glu_bf16(CUtensorMap* map, const void* base, uint64_t k, uint64_t n,
+                                 uint64_t mats);
+
 cudaError_t encode_tmap_w13_interleaved(CUtensorMap* map, const void* w13, uint64_t H, uint64_t I,
                                         uint64_t E);
 

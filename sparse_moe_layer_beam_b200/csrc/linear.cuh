@@ -1,0 +1,225 @@
+// linear.cuh - shared by the linear operator's kernels (linear.cu,
+// linear_pair.cu): parameters, the experts' segments, descriptors, TMA forms
+// and the activations.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace beam {
+namespace lin {
+
+enum Mode { kFwd, kDgrad, kWgrad };
+
+constexpr int kMaxE = 512;
+constexpr int kM = 128;       // rows of D per tile
+constexpr int kK = 64;        // contraction per pipeline stage
+constexpr int kRowGroup = 16; // row blocks that share a sweep over the columns
+constexpr int kBox = 64 * kK * 2;  // bytes of a 64 x 64 box
+
+struct LinParams {
+  const int32_t* offsets;  // [E + 1] or NULL
+  int E, rows;
+  int n_in, n_out, n_w;    // n_w: weight rows per expert (2 n_out for swiglu)
+  int cols;                // columns of D that exist (FWD n_out, else n_in)
+  int nk;                  // contraction steps (FWD, DGRAD)
+  int n_blk, m_blk;        // column tiles; row tiles of dW_e (WGRAD)
+  int box_a;               // rows per box of the row operand (FWD, DGRAD)
+  int act, fp16, out32;
+  const float* bias;       // [E][n_w] or NULL
+  const void* residual;    // [rows][n_out] or NULL
+  void* z;                 // [rows][n_w] or NULL
+  void* out;
+  unsigned* status;
+  int* next_tile;          // CTA pairs: counter of the tiles handed out
+};
+
+// ------------------------------------------------------------- the segments
+// Segment of expert e, clamped into the rows there are whatever offsets holds.
+__device__ __forceinline__ void segment(const LinParams& p, int e, int& lo, int& cnt) {
+  if (!p.offsets) {
+    lo = 0;
+    cnt = p.rows;
+    return;
+  }
+  lo = min(max(__ldg(p.offsets + e), 0), p.rows);
+  cnt = min(max(__ldg(p.offsets + e + 1), lo), p.rows) - lo;
+}
+
+// In shared memory: first row and row count of every expert, and the prefix
+// of its BLOCK-row blocks (rb[E]: all of them). THREADS threads call it.
+struct Segments {
+  int* lo;
+  int* cnt;
+  int* rb;
+};
+
+template <int THREADS, int BLOCK>
+__device__ __forceinline__ void build_segments(const LinParams& p, const Segments& s, int* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = (kMaxE + THREADS - 1) / THREADS;
+  int blocks[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    blocks[i] = 0;
+    if (e < p.E) {
+      int lo, cnt;
+      segment(p, e, lo, cnt);
+      s.lo[e] = lo;
+      s.cnt[e] = cnt;
+      blocks[i] = (cnt + BLOCK - 1) / BLOCK;
+    }
+    sum += blocks[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  int run = inc - sum;
+  for (int w = 0; w < warp; ++w) run += scratch[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    if (e < p.E) {
+      s.rb[e] = run;
+      run += blocks[i];
+      if (e == p.E - 1) s.rb[p.E] = run;
+    }
+  }
+  __syncthreads();
+}
+
+// The expert whose row blocks hold block q (rb[0] <= q < rb[E]).
+__device__ __forceinline__ int find_expert(const int* rb, int E, int q) {
+  int a = 0, b = E;  // rb[a] <= q < rb[b]
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (rb[m] <= q) a = m;
+    else b = m;
+  }
+  return a;
+}
+
+// -------------------------------------------------------------- descriptors
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+      "l"(policy)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: boxes of 64 (contraction) rows x 64
+// elements, 8 KB apart (leading offset), rows in groups of 8 that lie 1 KB
+// apart (stride offset). 16 contraction rows further: 2 KB.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kBox >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// FP32 sums of bf16 or fp16 products, M x N; an operand is K-major or MN-major.
+__device__ __forceinline__ uint32_t idesc_of(bool fp16, bool a_mn, bool b_mn, uint32_t M,
+                                             uint32_t N) {
+  const uint32_t fmt = fp16 ? 0u : 1u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// ----------------------------------------------------------------- epilogue
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// 1/2 (1 + erf(z / sqrt 2)) as a complement: relative accuracy down the tail.
+__device__ __forceinline__ float normal_cdf(float z) {
+  return 0.5f * erfcf(z * -0.70710678118654752f);
+}
+
+// 1/2 (1 + tanh(a)) = sigmoid(2 a) for a = sqrt(2/pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float tanh_gate(float z) {
+  return sigmoid_f(1.59576912160573071f * fmaf(0.044715f * z * z, z, z));
+}
+
+__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// act over N values. The choice is made once for all of them and the longer
+// formulas stay rolled: unrolled inside a switch per value they filled the
+// instruction cache and bounded the kernel (16384 x 5120 x 5120, act none:
+// 885 us against 590).
+template <int N>
+__device__ __forceinline__ void activate(int act, float* z) {
+  switch (act) {
+    case BEAM_MOE_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) z[j] = z[j] > 0.0f ? z[j] : 0.0f;
+      break;
+    case BEAM_MOE_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) z[j] *= normal_cdf(z[j]);
+      break;
+    case BEAM_MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < N; ++j) z[j] *= tanh_gate(z[j]);
+      break;
+    case BEAM_MOE_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) z[j] = silu_f(z[j]);
+      break;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t v, bool fp16) {
+  return fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+              : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// 4 consecutive elements at p (element index at, a multiple of 4).
+__device__ __forceinline__ void store4(void* p, int64_t at, const float* v, bool f32, bool fp16) {
+  if (f32)
+    reinterpret_cast<float4*>(static_cast<float*>(p) + at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at)[0] =
+        make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
+}
+
+__device__ __forceinline__ void load4(const void* p, int64_t at, float* v, bool f32, bool fp16) {
+  if (f32) {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    const float2 a = unpack16(u.x, fp16), b = unpack16(u.y, fp16);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+}
+
+}  // namespace lin
+
+// The product of one mode on CTA pairs (linear_pair.cu): a, b and p.out as
+// for the one-CTA kernel.
+cudaError_t launch_linear_pair(int mode, const lin::LinParams& p, const void* a, const void* b,
+                               cudaStream_t st);
+
+}  // namespace beam

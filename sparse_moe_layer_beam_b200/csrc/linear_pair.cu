@@ -1,0 +1,659 @@
+// linear_pair.cu - the linear operator's products on CTA pairs (tcgen05
+// cta_group::2), for experts with many rows. The same three products as
+// linear.cu, as D^T for the first two:
+//
+//   FWD    D[n][r] = sum_k W_e[n][k] X[r][k]      M: weight rows, N: rows of X
+//   DGRAD  D[k][r] = sum_n W_e[n][k] dZ[r][n]     M: weight columns
+//   WGRAD  D[n][k] = sum_r dZ[r][n] X[r][k]       M: rows of dW_e
+//
+// One MMA covers 256 x up to 256; each CTA of the pair holds 128 of M and half
+// of N in shared memory and 128 accumulator rows, double-buffered in TMEM, so
+// the epilogue of one tile overlaps the MMAs of the next. The rows of X and dZ
+// are N in FWD and DGRAD because N may be any multiple of 16: an expert's last
+// row block costs what it holds, where as M it would cost 128 rows (measured
+// at 8192 rows over 32 experts: a fifth of the tensor work).
+//
+// swiglu: a CTA's 128 weight rows are gate and up rows of 64 columns in turns
+// of 16, so a warp's 32 TMEM lanes hold 16 gate rows and their up rows, which
+// lanes exchange with one shuffle.
+//
+// WGRAD's last step of a segment holds rows of other experts. Each CTA takes
+// that step's copies on a barrier of its own, its warp 1 zeroes the rows in
+// both operands and releases the step to the MMA thread.
+//
+// Roles: warp 0 issues this CTA's TMA loads, counted on the even CTA's
+// barriers; warp 1 of the even CTA issues the pair's MMAs; warps 2-5 of each
+// CTA drain their TMEM. No load uses multicast. Every wait is bounded.
+#include <string.h>
+
+#include "linear.cuh"
+#include "ops.h"
+
+namespace beam {
+namespace {
+
+using namespace lin;
+
+constexpr int kThreads = 192;
+constexpr int kPair = 256;     // M and (most) N of a pair's tile
+constexpr int kGroup = 16;     // row blocks that share a sweep over the weights
+constexpr int kTileSlots = 8;  // tile indices between the fetching producer and the rest
+constexpr int kABytes = 128 * kK * 2;
+constexpr int kBBytes = 128 * kK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 6;
+constexpr int kBarBytes = 512;
+constexpr int kStoreBytes = 32 * 128;  // a warp's staged 32 x 64 block (WGRAD)
+
+template <int MODE>
+struct PairMem {
+  // behind the ring, WGRAD: 2 staged blocks per warp; else the segment table
+  static constexpr int kMore = MODE == kWgrad ? 4 * 2 * kStoreBytes : 4 * (3 * kMaxE + 16);
+  static constexpr int kBytes = 1024 + kStages * kStageBytes + kMore + kBarBytes;
+  static_assert(kBytes <= 232448, "dynamic shared memory above the sm_100 limit");
+};
+
+// ------------------------------------------------------------- TMA for pairs
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int32_t c0, int32_t c1, int32_t c2,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0,
+                                             int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// -------------------------------------------------------------------- tiles
+struct PairTile {
+  int e;
+  int m0;          // first row of M (swiglu: first of 128 columns of Y)
+  int row0, rows;  // FWD, DGRAD: rows of X (N of the tile)
+  int n0;          // WGRAD: first column
+  int k0, kcnt;    // WGRAD: the segment
+  int nk;          // contraction steps
+  bool once;       // the weight tile is read by this tile alone
+};
+
+// FWD, DGRAD: the row blocks of all experts, in order, go in groups of 16;
+// inside a group weight tile by weight tile, row blocks fastest. The pairs at
+// work at one time then share row blocks and weight tiles through L2, and
+// experts with few rows (bound by their weights' bytes) run beside experts
+// with many (bound by the tensor cores). WGRAD: expert by expert, groups of 16
+// column tiles, row tile by row tile.
+template <int MODE>
+__device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const Segments& s,
+                                                int m_step) {
+  PairTile d;
+  const int m_blk = p.m_blk;
+  int blks, local;
+  if (MODE == kWgrad) {
+    const int per = m_blk * p.n_blk;
+    d.e = t / per;
+    local = t - d.e * per;
+    blks = p.n_blk;
+  } else {
+    local = t;
+    blks = s.rb[p.E];
+  }
+  const int g = local / (kGroup * m_blk);
+  const int in_g = min(kGroup, blks - g * kGroup);
+  const int rem = local - g * kGroup * m_blk;
+  const int mb = rem / in_g;
+  const int nb = g * kGroup + rem - mb * in_g;
+  d.m0 = mb * m_step;
+  if (MODE == kWgrad) {
+    segment(p, d.e, d.k0, d.kcnt);
+    d.nk = (d.kcnt + kK - 1) / kK;
+    d.n0 = nb * kPair;
+    d.row0 = d.rows = 0;
+    d.once = false;
+  } else {
+    d.e = find_expert(s.rb, p.E, nb);
+    const int i0 = (nb - s.rb[d.e]) * kPair;
+    d.row0 = s.lo[d.e] + i0;
+    d.rows = min(kPair, s.cnt[d.e] - i0);
+    d.nk = p.nk;
+    d.n0 = d.k0 = d.kcnt = 0;
+    d.once = s.rb[d.e + 1] - s.rb[d.e] == 1;
+  }
+  return d;
+}
+
+__device__ __forceinline__ float load1(const void* p, int64_t at, bool f32, bool fp16) {
+  if (f32) return static_cast<const float*>(p)[at];
+  return fp16 ? __half2float(static_cast<const __half*>(p)[at])
+              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+
+template <class T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// n <= N values, one per row, into one column of a row-major matrix. A warp's
+// lanes hold neighbouring columns: 64 or 128 bytes of a row per instruction.
+template <int N, class T>
+__device__ __forceinline__ void store_rows(void* p, int64_t at, int64_t ld, int n, const float* v) {
+  T* o = static_cast<T*>(p) + at;
+#pragma unroll
+  for (int j = 0; j < N; ++j, o += ld)
+    if (j < n) *o = narrow<T>(v[j]);
+}
+
+template <int N>
+__device__ __forceinline__ void store_rows(void* p, int64_t at, int64_t ld, int n, const float* v,
+                                           bool f32, bool fp16) {
+  if (f32) store_rows<N, float>(p, at, ld, n, v);
+  else if (fp16) store_rows<N, __half>(p, at, ld, n, v);
+  else store_rows<N, __nv_bfloat16>(p, at, ld, n, v);
+}
+
+// N rows (from row r0 of the tile) of one column of Y; v: act(Z).
+template <int N>
+__device__ __forceinline__ void finish_rows(const LinParams& p, const PairTile& t, int col, int r0,
+                                            float* v) {
+  const int n = min(N, t.rows - r0);
+  const int64_t at = (int64_t)(t.row0 + r0) * p.n_out + col;
+  if (p.residual) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < n) v[j] += load1(p.residual, at + (int64_t)j * p.n_out, p.out32, p.fp16);
+  }
+  store_rows<N>(p.out, at, p.n_out, n, v, p.out32, p.fp16);
+}
+
+template <int MODE, bool GLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
+                       const __grid_constant__ CUtensorMap tm_b,
+                       const __grid_constant__ CUtensorMap tm_c, const LinParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* more = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(more + PairMem<MODE>::kMore);
+  uint64_t* empty = full + kStages;
+  uint64_t* tail = empty + kStages;  // WGRAD: a segment's last step has landed here
+  uint64_t* tfull = tail + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* tsfull = drain + 1;             // [kTileSlots] an index is in the ring
+  uint64_t* tsempty = tsfull + kTileSlots;  // [kTileSlots] every reader has it (even CTA)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tsempty + kTileSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* ring = abort_flag + 1;      // [kTileSlots] tile index, -1: no more
+  static_assert((3 * kStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots <= kBarBytes,
+                "barrier area");
+  // readers of an index: the odd CTA's producer, the MMA warp (WGRAD: the odd
+  // CTA's warp 1 too) and the four epilogue warps of each CTA
+  constexpr int kTileReaders = (MODE == kWgrad ? 3 : 2) + 2 * 4;
+  int* tab = reinterpret_cast<int*>(more);
+  const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues MMAs
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      // WGRAD: a tail step is released by both CTAs' warps 1, the others by
+      // the even CTA's producer alone, which arrives twice
+      mbar_init(&full[s], MODE == kWgrad ? 2 : 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * 128);
+    }
+    mbar_init(drain, 1);
+    for (int s = 0; s < kTileSlots; ++s) {
+      mbar_init(&tsfull[s], 1);
+      mbar_init(&tsempty[s], kTileReaders);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_c);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  if (MODE != kWgrad) build_segments<kThreads, kPair>(p, seg, tab + 3 * kMaxE + 1);
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int m_step = GLU ? 128 : kPair;
+  const int total = MODE == kWgrad ? p.E * p.m_blk * p.n_blk : seg.rb[p.E] * p.m_blk;
+
+  // Tiles are handed out in order at run time (they differ in rows, and in
+  // order their operands stay in L2): the even CTA's producer takes the next
+  // index from a counter and publishes it to every role of both CTAs. -1: no
+  // tiles left; -2: a wait gave up (the role stops).
+  int tslot = 0;
+  uint32_t tphase = 0;
+  auto next_slot = [&]() {
+    if (++tslot == kTileSlots) {
+      tslot = 0;
+      tphase ^= 1u;
+    }
+  };
+  auto publish_tile = [&](int taken) -> int {
+    // the readers' arrivals (some from the other CTA) come before the rewrite
+    if (!mbar_wait(&tsempty[tslot], tphase ^ 1u, abort_flag, p.status, kFlagProducer, 1000000000ull,
+                   true))
+      return -2;
+    const int tile = taken < total ? taken : -1;
+    ring[tslot] = tile;
+    st_cluster_u32(mapa_shared(smem_addr((const void*)&ring[tslot]), 1), (uint32_t)tile);
+    mbar_arrive(&tsfull[tslot]);
+    mbar_arrive_cluster(mapa_shared(smem_addr(&tsfull[tslot]), 1));
+    next_slot();
+    return tile;
+  };
+  // whole_warp: all 32 lanes read and lane 0 arrives for them, else one does.
+  auto read_tile = [&](uint32_t flag, bool whole_warp) -> int {
+    const bool got = mbar_wait(&tsfull[tslot], tphase, abort_flag, p.status, flag, 1000000000ull,
+                               true);
+    if (whole_warp ? !__all_sync(0xffffffffu, got) : !got) return -2;
+    const int tile = ring[tslot];
+    if (whole_warp) __syncwarp();  // every lane has read the slot
+    if (!whole_warp || lane == 0)
+      mbar_arrive_cluster(mapa_shared(smem_addr(&tsempty[tslot]), 0));
+    next_slot();
+    return tile;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      const uint64_t pol_stream = policy_evict_first();
+      const uint64_t pol_keep = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      int taken = leader ? atomicAdd(p.next_tile, 1) : 0;
+      while (ok) {
+        const int ti = leader ? publish_tile(taken) : read_tile(kFlagProducer, false);
+        if (ti < 0) break;
+        if (leader) taken = atomicAdd(p.next_tile, 1);  // used at the next tile
+        const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
+        const int half = ((t.rows + 15) & ~15) >> 1;  // this CTA's rows of N: 8 .. 128
+        const bool box64 = half <= 64;
+        const CUtensorMap* tmx = box64 ? &tm_c : &tm_b;  // boxes of 64 or 128 rows
+        const int xrow = t.row0 + (int)rank * half;
+        const uint64_t pol_w = t.once ? pol_stream : pol_keep;
+        const int m0 = t.m0 + (int)rank * (m_step / 2);
+        for (int k = 0; k < t.nk; ++k) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kFlagProducer)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * kStageBytes;
+          uint8_t* sb = sa + kABytes;
+          const uint32_t lead = mapa_shared(smem_addr(&full[stage]), 0);
+          if (MODE == kWgrad) {
+            const bool last = t.kcnt - k * kK < kK;
+            if (last) {
+              mbar_arrive_expect_tx(&tail[stage], kStageBytes);
+            } else if (leader) {
+              mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+              mbar_arrive(&full[stage]);
+            }
+            const uint32_t bar = last ? mapa_shared(smem_addr(&tail[stage]), rank) : lead;
+            const int r = t.k0 + k * kK;
+            const int n0 = t.n0 + (int)rank * 128;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              tma_load_2d_pair(sa + b * kBox, &tm_a, bar, m0 + b * 64, r, pol_keep);
+              tma_load_2d_pair(sb + b * kBox, &tm_b, bar, n0 + b * 64, r, pol_keep);
+            }
+          } else {
+            if (leader)
+              mbar_arrive_expect_tx(&full[stage], 2u * (kABytes + (box64 ? 64 : 128) * kK * 2));
+            const int kx = k * kK;
+            if (MODE == kDgrad) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                tma_load_3d_pair(sa + b * kBox, &tm_a, lead, m0 + b * 64, kx, t.e, pol_w);
+            } else if (GLU) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                tma_load_4d_pair(sa + b * (kABytes / 4), &tm_a, lead, kx, m0 + b * 16, 0, t.e,
+                                 pol_w);
+            } else {
+              tma_load_3d_pair(sa, &tm_a, lead, kx, m0, t.e, pol_w);
+            }
+            tma_load_2d_pair(sb, tmx, lead, kx, xrow, pol_keep);
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // The even CTA's full barriers count both CTAs' copies: wait for the
+      // last ones to land before either CTA can leave.
+      if (leader) {
+        const int64_t from = issued > kStages ? issued - kStages : 0;
+        for (int64_t i = from; i < issued; ++i)
+          mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1), nullptr, nullptr, 0u,
+                    100000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // The even CTA's warp issues the pair's MMAs; in WGRAD both CTAs' zero
+    // what lies behind a segment in its last step.
+    if (leader || MODE == kWgrad) {
+      int stage = 0;
+      uint32_t phase = 0, tail_phase = 0;  // tail_phase: a bit per stage
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      while (ok) {
+        const int ti = read_tile(kFlagMma, true);
+        if (ti < 0) break;
+        const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
+        if (t.nk == 0) continue;  // an expert without rows: the epilogue takes zeros
+        uint32_t idesc = 0, d = 0;
+        if (leader) {
+          idesc = idesc_of(p.fp16, MODE != kFwd, MODE == kWgrad, kPair,
+                           MODE == kWgrad ? kPair : (uint32_t)((t.rows + 15) & ~15));
+          ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag,
+                                                 p.status, kFlagMma));
+          if (!ok) break;
+          tc_fence_after();
+          d = tmem_base + (uint32_t)(acc * kPair);
+        }
+        for (int k = 0; k < t.nk; ++k) {
+          uint8_t* s_a = smem + stage * kStageBytes;
+          int k16 = kK / 16;
+          if (MODE == kWgrad) {
+            const int rem = t.kcnt - k * kK;  // rows of the segment in this step
+            if (rem < kK) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&tail[stage], (tail_phase >> stage) & 1u,
+                                                     abort_flag, p.status, kFlagMma));
+              if (!ok) break;
+              tail_phase ^= 1u << stage;
+              k16 = (rem + 15) / 16;
+              const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
+              uint4* base = reinterpret_cast<uint4*>(s_a);
+              for (int i = lane; i < dirty * 8 * 4; i += 32) {
+                const int box = i / (dirty * 8), j = i - box * dirty * 8;
+                base[box * (kBox / 16) + rem * 8 + j] = make_uint4(0, 0, 0, 0);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&full[stage]), 0));
+            }
+          }
+          if (leader) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.status,
+                                                   kFlagMma, 1000000000ull, MODE == kWgrad));
+            if (!ok) break;
+            if (lane == 0) {
+              tc_fence_after();
+              const uint32_t sa = smem_addr(s_a), sb = sa + kABytes;
+              const uint64_t da = MODE == kFwd ? smem_desc_k_sw128(sa) : smem_desc_mn_sw128(sa);
+              const uint64_t db = MODE == kWgrad ? smem_desc_mn_sw128(sb) : smem_desc_k_sw128(sb);
+              constexpr uint32_t kStepA = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
+              constexpr uint32_t kStepB = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
+              for (int q = 0; q < k16; ++q)
+                umma_bf16_pair(d, da + kStepA * q, db + kStepB * q, idesc, k | q);
+              umma_commit_pair(&empty[stage], 0x3);
+            }
+            __syncwarp();
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (leader) {
+          if (lane == 0) umma_commit_pair(&tfull[acc], 0x3);
+          __syncwarp();
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+      }
+      if (leader && lane == 0) {
+        // Every MMA of the pair completes before TMEM is released.
+        umma_commit_pair(drain, 0x1);
+        mbar_wait(drain, 0, nullptr, nullptr, 0u, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // TMEM lane quadrant of this warp
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int staged = 0;  // WGRAD: the staging block in turn
+    for (;;) {
+      const int ti = read_tile(kFlagEpilogue, true);
+      if (ti < 0) break;
+      const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
+      const bool none = t.nk == 0;
+      if (!none) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status,
+                                               kFlagEpilogue)))
+          break;
+        tc_fence_after();
+      }
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kPair);
+      if (MODE == kWgrad) {
+        // 32 rows x 64 columns at a time: rounded, staged in the 128-byte
+        // swizzle TMA expects, stored by TMA (which cuts off what lies behind
+        // the matrix). Stores straight from registers touch 32 rows per
+        // instruction and bound the kernel when segments are short.
+        const int row = t.m0 + (int)rank * 128 + q * 32;
+        for (int c0 = 0; c0 < kPair && t.n0 + c0 < p.n_in && row < p.n_w; c0 += 64) {
+          uint8_t* buf = more + (q * 2 + staged) * kStoreBytes;
+          uint32_t v[4][16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[i][j] = 0u;
+            } else {
+              tmem_ld16(tb + c0 + i * 16, v[i]);
+            }
+          }
+          if (!none) tmem_ld_wait();
+          // the store before the last has read its block
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* f = reinterpret_cast<const float*>(&v[i >> 1][(i & 1) * 8]);
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(pack16(f[0], f[1], p.fp16), pack16(f[2], f[3], p.fp16),
+                           pack16(f[4], f[5], p.fp16), pack16(f[6], f[7], p.fp16));
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_c, buf, t.n0 + c0, row, t.e);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          staged ^= 1;
+        }
+      } else if (GLU) {
+        // lanes 0-15: gate rows, 16-31: up rows of 16 columns of Y
+        const int col = t.m0 + (int)rank * 64 + q * 16 + (lane & 15);
+        const bool live = col < p.n_out;
+        const int wrow = (lane < 16 ? 0 : p.n_out) + col;  // this lane's weight row
+        const float bias = p.bias && live ? __ldg(p.bias + (int64_t)t.e * p.n_w + wrow) : 0.0f;
+        for (int c0 = 0; c0 < t.rows; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(tb + c0, v);
+          tmem_ld_wait();
+          float* f = reinterpret_cast<float*>(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] += bias;
+          if (p.z && live) {
+            store_rows<16>(p.z, (int64_t)(t.row0 + c0) * p.n_w + wrow, p.n_w, t.rows - c0, f,
+                           false, p.fp16);
+          }
+          float g[8], u[8];  // 8 of the 16 rows: the lower half's first 8, the upper's last
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? f[8 + j] : f[j], 16);
+            g[j] = lane < 16 ? f[j] : other;
+            u[j] = lane < 16 ? other : f[8 + j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = silu_f(g[j]) * u[j];
+          if (live) finish_rows<8>(p, t, col, c0 + (lane >> 4) * 8, g);
+        }
+      } else {
+        const int col = t.m0 + (int)rank * 128 + q * 32 + lane;
+        const bool live = col < p.cols;
+        const float bias =
+            MODE == kFwd && p.bias && live ? __ldg(p.bias + (int64_t)t.e * p.n_w + col) : 0.0f;
+        for (int c0 = 0; c0 < t.rows; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(tb + c0, v);
+          tmem_ld_wait();
+          float* f = reinterpret_cast<float*>(v);
+          if (!live) continue;
+          if (MODE == kDgrad) {
+            store_rows<16>(p.out, (int64_t)(t.row0 + c0) * p.n_in + col, p.n_in, t.rows - c0, f,
+                           false, p.fp16);
+            continue;
+          }
+          if (MODE == kFwd) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] += bias;
+            if (p.z)
+              store_rows<16>(p.z, (int64_t)(t.row0 + c0) * p.n_w + col, p.n_w, t.rows - c0, f,
+                             false, p.fp16);
+            activate<16>(p.act, f);
+            finish_rows<16>(p, t, col, c0, f);
+          }
+        }
+      }
+      if (!none) {
+        tc_fence_before();
+        mbar_arrive_cluster(mapa_shared(smem_addr(&tempty[acc]), 0));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    if (MODE == kWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // both CTAs done with TMEM and with each other's memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int MODE, bool GLU>
+cudaError_t run_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                      const LinParams& p, cudaStream_t st) {
+  // Per device: the shared-memory attribute and the number of CTA pairs that
+  // can be resident at once (a pair needs two SMs of one GPC).
+  static PerDevice pairs;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = PairMem<MODE>::kBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int resident = 0;
+  cudaError_t err = per_device(pairs, &resident, [&cfg](int* v) {
+    cudaError_t e =
+        cudaFuncSetAttribute(linear_pair_kernel<MODE, GLU>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, PairMem<MODE>::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t probe = cfg;
+    probe.gridDim = dim3((unsigned)(device_sm_count() & ~1));
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, linear_pair_kernel<MODE, GLU>, &probe);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    *v = clusters < device_sm_count() / 2 ? clusters : device_sm_count() / 2;
+    return cudaSuccess;
+  });
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3((unsigned)(2 * resident));
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE, GLU>, ta, tb, tc, p);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pair(int mode, const LinParams& base, const void* a, const void* b,
+                               cudaStream_t st) {
+  LinParams p = base;
+  const uint64_t R = p.rows, E = p.E;
+  // words of the status area, zero at the call's start; a launch each
+  p.next_tile = reinterpret_cast<int*>(p.status) + kTileCounterWord + mode;
+  const bool glu = mode == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
+  CUtensorMap ta, tb, tc;
+  cudaError_t err;
+  if (mode == kWgrad) {
+    p.m_blk = (p.n_w + kPair - 1) / kPair;
+    p.n_blk = (p.n_in + kPair - 1) / kPair;
+    err = encode_tmap_2d_bf16(&ta, a, p.n_w, R, 64, 64);
+    if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, b, p.n_in, R, 64, 64);
+    if (err == cudaSuccess) err = encode_tmap_3d_bf16(&tc, p.out, p.n_in, p.n_w, E, 64, 32);
+    if (err != cudaSuccess) return err;
+    return run_pairs<kWgrad, false>(ta, tb, tc, p, st);
+  }
+  // a: rows of X or dZ, b: the weights; on pairs the weights are the A operand
+  const uint64_t kc = mode == kFwd ? p.n_in : p.n_w;
+  p.nk = (int)((kc + kK - 1) / kK);
+  p.m_blk = glu ? (p.n_out + 127) / 128 : (p.cols + kPair - 1) / kPair;
+  if (glu)
+    err = encode_tmap_glu_bf16(&ta, b, p.n_in, p.n_out, E);
+  else
+    err = encode_tmap_3d_bf16(&ta, b, p.n_in, p.n_w, E, 64, mode == kDgrad ? 64 : 128);
+  if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, a, kc, R, 64, 128);
+  if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tc, a, kc, R, 64, 64);
+  if (err != cudaSuccess) return err;
+  if (mode == kDgrad) return run_pairs<kDgrad, false>(ta, tb, tc, p, st);
+  return glu ? run_pairs<kFwd, true>(ta, tb, tc, p, st) : run_pairs<kFwd, false>(ta, tb, tc, p, st);
+}
+
+}  // namespace beam

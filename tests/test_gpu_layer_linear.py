@@ -97,7 +97,10 @@ CASES = [
     ([0, 0, 0], 5, 64, 64, "gelu", "bf16"),
     ([2] * 60 + [0] * 4 + [40], 0, 320, 328, "swiglu", "bf16"),  # 128-column tiles
     ([100] * 9 + [517], 1, 256, 2600, "silu", "bf16"),           # 256-column tiles
-    ([700, 0, 2300], 0, 1032, 1288, "swiglu", "fp16"),
+    ([700, 0, 2300], 0, 1032, 1288, "swiglu", "fp16"),           # CTA pairs from here on
+    ([129, 300, 0, 513], 2, 1032, 5128, "gelu", "bf16"),
+    ([1400], 0, 1096, 3208, "none", "fp16"),
+    ([400, 100, 1, 900], 0, 2312, 1672, "swiglu", "bf16"),
 ]
 
 
