@@ -49,8 +49,9 @@ __device__ __forceinline__ void segment(const LinParams& p, int e, int& lo, int&
   cnt = min(max(__ldg(p.offsets + e + 1), lo), p.rows) - lo;
 }
 
-// In shared memory: first row and row count of every expert, and the prefix
-// of its BLOCK-row blocks (rb[E]: all of them). THREADS threads call it.
+// In shared memory: first row and row count of every expert (unless lo is
+// NULL), and the prefix of its BLOCK-row blocks (rb[E]: all of them). THREADS
+// threads call it.
 struct Segments {
   int* lo;
   int* cnt;
@@ -69,8 +70,10 @@ __device__ __forceinline__ void build_segments(const LinParams& p, const Segment
     if (e < p.E) {
       int lo, cnt;
       segment(p, e, lo, cnt);
-      s.lo[e] = lo;
-      s.cnt[e] = cnt;
+      if (s.lo) {
+        s.lo[e] = lo;
+        s.cnt[e] = cnt;
+      }
       blocks[i] = (cnt + BLOCK - 1) / BLOCK;
     }
     sum += blocks[i];

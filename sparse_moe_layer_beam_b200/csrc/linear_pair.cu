@@ -18,8 +18,10 @@
 // lanes exchange with one shuffle.
 //
 // WGRAD's last step of a segment holds rows of other experts. Each CTA takes
-// that step's copies on a barrier of its own, its warp 1 zeroes the rows in
-// both operands and releases the step to the MMA thread.
+// that step's copies on a barrier of its own; a warp of its own (6) zeroes the
+// rows in both operands as soon as they have landed, ahead of the MMAs, and
+// releases the step to the MMA thread (done by the MMA warp in turn it cost
+// 160 of 1260 us at 512 rows an expert).
 //
 // Roles: warp 0 issues this CTA's TMA loads, counted on the even CTA's
 // barriers; warp 1 of the even CTA issues the pair's MMAs; warps 2-5 of each
@@ -34,7 +36,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192;   // WGRAD: a warp more, see below
 constexpr int kPair = 256;     // M and (most) N of a pair's tile
 constexpr int kGroup = 16;     // row blocks that share a sweep over the weights
 constexpr int kTileSlots = 8;  // tile indices between the fetching producer and the rest
@@ -47,8 +49,9 @@ constexpr int kStoreBytes = 32 * 128;  // a warp's staged 32 x 64 block (WGRAD)
 
 template <int MODE>
 struct PairMem {
+  static constexpr int kBlock = MODE == kWgrad ? kThreads + 32 : kThreads;
   // behind the ring, WGRAD: 2 staged blocks per warp; else the segment table
-  static constexpr int kMore = MODE == kWgrad ? 4 * 2 * kStoreBytes : 4 * (3 * kMaxE + 16);
+  static constexpr int kMore = MODE == kWgrad ? 4 * 2 * kStoreBytes : 4 * (kMaxE + 1 + 7);
   static constexpr int kBytes = 1024 + kStages * kStageBytes + kMore + kBarBytes;
   static_assert(kBytes <= 232448, "dynamic shared memory above the sm_100 limit");
 };
@@ -83,6 +86,20 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+
+// One lane of a converged warp, in the form the compiler knows to be one: the
+// loops around it stay uniform, so that descriptors and addresses live in
+// uniform registers. Issued from inside an `if (lane == 0)` each MMA cost the
+// thread some 70 cycles of register moves, and a step more than its MMAs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // -------------------------------------------------------------------- tiles
 struct PairTile {
@@ -131,8 +148,10 @@ __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const
   } else {
     d.e = find_expert(s.rb, p.E, nb);
     const int i0 = (nb - s.rb[d.e]) * kPair;
-    d.row0 = s.lo[d.e] + i0;
-    d.rows = min(kPair, s.cnt[d.e] - i0);
+    int lo, cnt;
+    segment(p, d.e, lo, cnt);
+    d.row0 = lo + i0;
+    d.rows = min(kPair, cnt - i0);
     d.nk = p.nk;
     d.n0 = d.k0 = d.kcnt = 0;
     d.once = s.rb[d.e + 1] - s.rb[d.e] == 1;
@@ -190,7 +209,7 @@ __device__ __forceinline__ void finish_rows(const LinParams& p, const PairTile& 
 }
 
 template <int MODE, bool GLU>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b,
                        const __grid_constant__ CUtensorMap tm_c, const LinParams p) {
@@ -211,18 +230,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* ring = abort_flag + 1;      // [kTileSlots] tile index, -1: no more
   static_assert((3 * kStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots <= kBarBytes,
                 "barrier area");
-  // readers of an index: the odd CTA's producer, the MMA warp (WGRAD: the odd
-  // CTA's warp 1 too) and the four epilogue warps of each CTA
-  constexpr int kTileReaders = (MODE == kWgrad ? 3 : 2) + 2 * 4;
+  // readers of an index: the odd CTA's producer, the MMA thread and, of each
+  // CTA, the four epilogue warps (WGRAD: and the cleaner)
+  constexpr int kTileReaders = 2 + 2 * (MODE == kWgrad ? 5 : 4);
   int* tab = reinterpret_cast<int*>(more);
-  const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
+  const Segments seg = {nullptr, nullptr, tab};
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues MMAs
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      // WGRAD: a tail step is released by both CTAs' warps 1, the others by
+      // WGRAD: a tail step is released by both CTAs' cleaners, the others by
       // the even CTA's producer alone, which arrives twice
       mbar_init(&full[s], MODE == kWgrad ? 2 : 1);
       mbar_init(&empty[s], 1);
@@ -247,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
   }
-  if (MODE != kWgrad) build_segments<kThreads, kPair>(p, seg, tab + 3 * kMaxE + 1);
+  if (MODE != kWgrad) build_segments<kThreads, kPair>(p, seg, tab + kMaxE + 1);
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_base = (uint32_t)uniform((int)*tmem_holder);
   const int m_step = GLU ? 128 : kPair;
   const int total = MODE == kWgrad ? p.E * p.m_blk * p.n_blk : seg.rb[p.E] * p.m_blk;
 
@@ -269,193 +288,218 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto publish_tile = [&](int taken) -> int {
     // the readers' arrivals (some from the other CTA) come before the rewrite
-    if (!mbar_wait(&tsempty[tslot], tphase ^ 1u, abort_flag, p.status, kFlagProducer, 1000000000ull,
-                   true))
-      return -2;
+    const bool got = mbar_wait(&tsempty[tslot], tphase ^ 1u, abort_flag, p.status, kFlagProducer,
+                               1000000000ull, true);
+    if (!__all_sync(0xffffffffu, got)) return -2;
     const int tile = taken < total ? taken : -1;
-    ring[tslot] = tile;
-    st_cluster_u32(mapa_shared(smem_addr((const void*)&ring[tslot]), 1), (uint32_t)tile);
-    mbar_arrive(&tsfull[tslot]);
-    mbar_arrive_cluster(mapa_shared(smem_addr(&tsfull[tslot]), 1));
+    if (lane == 0) {
+      ring[tslot] = tile;
+      st_cluster_u32(mapa_shared(smem_addr((const void*)&ring[tslot]), 1), (uint32_t)tile);
+      mbar_arrive(&tsfull[tslot]);
+      mbar_arrive_cluster(mapa_shared(smem_addr(&tsfull[tslot]), 1));
+    }
     next_slot();
     return tile;
   };
-  // whole_warp: all 32 lanes read and lane 0 arrives for them, else one does.
-  auto read_tile = [&](uint32_t flag, bool whole_warp) -> int {
+  auto take_tile = [&]() -> int {
+    return uniform(lane == 0 ? atomicAdd(p.next_tile, 1) : 0);
+  };
+  // All 32 lanes read, lane 0 arrives for them.
+  auto read_tile = [&](uint32_t flag) -> int {
     const bool got = mbar_wait(&tsfull[tslot], tphase, abort_flag, p.status, flag, 1000000000ull,
                                true);
-    if (whole_warp ? !__all_sync(0xffffffffu, got) : !got) return -2;
-    const int tile = ring[tslot];
-    if (whole_warp) __syncwarp();  // every lane has read the slot
-    if (!whole_warp || lane == 0)
-      mbar_arrive_cluster(mapa_shared(smem_addr(&tsempty[tslot]), 0));
+    if (!__all_sync(0xffffffffu, got)) return -2;
+    const int tile = uniform(ring[tslot]);
+    __syncwarp();  // every lane has read the slot
+    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&tsempty[tslot]), 0));
     next_slot();
     return tile;
+  };
+  // A wait of the whole warp.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity, uint32_t flag, bool cluster) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, flag,
+                                             1000000000ull, cluster));
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------ TMA producer
-      const uint64_t pol_stream = policy_evict_first();
-      const uint64_t pol_keep = policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      int taken = leader ? atomicAdd(p.next_tile, 1) : 0;
-      while (ok) {
-        const int ti = leader ? publish_tile(taken) : read_tile(kFlagProducer, false);
-        if (ti < 0) break;
-        if (leader) taken = atomicAdd(p.next_tile, 1);  // used at the next tile
-        const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
-        const int half = ((t.rows + 15) & ~15) >> 1;  // this CTA's rows of N: 8 .. 128
-        const bool box64 = half <= 64;
-        const CUtensorMap* tmx = box64 ? &tm_c : &tm_b;  // boxes of 64 or 128 rows
-        const int xrow = t.row0 + (int)rank * half;
-        const uint64_t pol_w = t.once ? pol_stream : pol_keep;
-        const int m0 = t.m0 + (int)rank * (m_step / 2);
-        for (int k = 0; k < t.nk; ++k) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kFlagProducer)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          const uint32_t lead = mapa_shared(smem_addr(&full[stage]), 0);
+    // -------------------------------------------------------- TMA producer
+    const uint64_t pol_stream = policy_evict_first();
+    const uint64_t pol_keep = policy_evict_normal();
+    const bool one = elect_one();
+    const uint32_t full0 = mapa_shared(smem_addr(full), 0);     // the even CTA's
+    const uint32_t tail0 = mapa_shared(smem_addr(tail), rank);  // this CTA's
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    // an index is published a tile ahead and taken two ahead, so that neither
+    // the atomic's latency nor the other CTA's is waited for
+    int taken = leader ? take_tile() : 0;
+    int ti = leader ? publish_tile(taken) : read_tile(kFlagProducer);
+    if (leader) taken = take_tile();
+    for (int next; ti >= 0 && ok; ti = next) {
+      next = -1;
+      if (leader) {
+        next = publish_tile(taken);
+        taken = take_tile();
+      }
+      const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
+      const int half = ((t.rows + 15) & ~15) >> 1;  // this CTA's rows of N: 8 .. 128
+      const bool box64 = half <= 64;
+      const CUtensorMap* tmx = box64 ? &tm_c : &tm_b;  // boxes of 64 or 128 rows
+      const int xrow = t.row0 + (int)rank * half;
+      const uint32_t tx = MODE == kWgrad ? 2 * kStageBytes
+                                         : 2u * (kABytes + (box64 ? 64 : 128) * kK * 2);
+      const uint64_t pol_w = t.once ? pol_stream : pol_keep;
+      const int m0 = t.m0 + (int)rank * (m_step / 2), n0 = t.n0 + (int)rank * 128;
+      const int nk = uniform(t.nk);
+      for (int k = 0; k < nk; ++k) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, kFlagProducer, false)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * kStageBytes;
+        uint8_t* sb = sa + kABytes;
+        uint32_t bar = full0 + 8 * stage;
+        const int kx = k * kK;
+        if (one) {
           if (MODE == kWgrad) {
-            const bool last = t.kcnt - k * kK < kK;
-            if (last) {
+            if (t.kcnt - kx < kK) {  // a segment's last step: the cleaner's
+              bar = tail0 + 8 * stage;
               mbar_arrive_expect_tx(&tail[stage], kStageBytes);
             } else if (leader) {
-              mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+              mbar_arrive_expect_tx(&full[stage], tx);
               mbar_arrive(&full[stage]);
             }
-            const uint32_t bar = last ? mapa_shared(smem_addr(&tail[stage]), rank) : lead;
-            const int r = t.k0 + k * kK;
-            const int n0 = t.n0 + (int)rank * 128;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              tma_load_2d_pair(sa + b * kBox, &tm_a, bar, m0 + b * 64, r, pol_keep);
-              tma_load_2d_pair(sb + b * kBox, &tm_b, bar, n0 + b * 64, r, pol_keep);
+              tma_load_2d_pair(sa + b * kBox, &tm_a, bar, m0 + b * 64, t.k0 + kx, pol_keep);
+              tma_load_2d_pair(sb + b * kBox, &tm_b, bar, n0 + b * 64, t.k0 + kx, pol_keep);
             }
           } else {
-            if (leader)
-              mbar_arrive_expect_tx(&full[stage], 2u * (kABytes + (box64 ? 64 : 128) * kK * 2));
-            const int kx = k * kK;
+            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
             if (MODE == kDgrad) {
 #pragma unroll
               for (int b = 0; b < 2; ++b)
-                tma_load_3d_pair(sa + b * kBox, &tm_a, lead, m0 + b * 64, kx, t.e, pol_w);
+                tma_load_3d_pair(sa + b * kBox, &tm_a, bar, m0 + b * 64, kx, t.e, pol_w);
             } else if (GLU) {
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                tma_load_4d_pair(sa + b * (kABytes / 4), &tm_a, lead, kx, m0 + b * 16, 0, t.e,
+                tma_load_4d_pair(sa + b * (kABytes / 4), &tm_a, bar, kx, m0 + b * 16, 0, t.e,
                                  pol_w);
             } else {
-              tma_load_3d_pair(sa, &tm_a, lead, kx, m0, t.e, pol_w);
+              tma_load_3d_pair(sa, &tm_a, bar, kx, m0, t.e, pol_w);
             }
-            tma_load_2d_pair(sb, tmx, lead, kx, xrow, pol_keep);
-          }
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+            tma_load_2d_pair(sb, tmx, bar, kx, xrow, pol_keep);
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // The even CTA's full barriers count both CTAs' copies: wait for the
-      // last ones to land before either CTA can leave.
-      if (leader) {
-        const int64_t from = issued > kStages ? issued - kStages : 0;
-        for (int64_t i = from; i < issued; ++i)
-          mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1), nullptr, nullptr, 0u,
-                    100000000ull);
-      }
+      if (!leader && ok) next = read_tile(kFlagProducer);
+    }
+    // The even CTA's full barriers count both CTAs' copies: wait for the
+    // last ones to land before either CTA can leave.
+    if (leader && lane == 0) {
+      const int64_t from = issued > kStages ? issued - kStages : 0;
+      for (int64_t i = from; i < issued; ++i)
+        mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1), nullptr, nullptr, 0u,
+                  100000000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // The even CTA's warp issues the pair's MMAs; in WGRAD both CTAs' zero
-    // what lies behind a segment in its last step.
-    if (leader || MODE == kWgrad) {
+    if (leader) {
+      // --------------------------------------------------------- MMA issuer
+      const bool one = elect_one();
+      const uint32_t smem0 = smem_addr(smem);
+      const uint64_t desc_a = MODE == kFwd ? smem_desc_k_sw128(smem0) : smem_desc_mn_sw128(smem0);
+      const uint64_t desc_b = MODE == kWgrad ? smem_desc_mn_sw128(smem0 + kABytes)
+                                             : smem_desc_k_sw128(smem0 + kABytes);
+      constexpr uint32_t kStepA = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
+      constexpr uint32_t kStepB = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
       int stage = 0;
-      uint32_t phase = 0, tail_phase = 0;  // tail_phase: a bit per stage
+      uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       while (ok) {
-        const int ti = read_tile(kFlagMma, true);
+        const int ti = read_tile(kFlagMma);
         if (ti < 0) break;
         const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
-        if (t.nk == 0) continue;  // an expert without rows: the epilogue takes zeros
-        uint32_t idesc = 0, d = 0;
-        if (leader) {
-          idesc = idesc_of(p.fp16, MODE != kFwd, MODE == kWgrad, kPair,
-                           MODE == kWgrad ? kPair : (uint32_t)((t.rows + 15) & ~15));
-          ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag,
-                                                 p.status, kFlagMma));
-          if (!ok) break;
+        const int nk = uniform(t.nk);
+        if (nk == 0) continue;  // an expert without rows: the epilogue takes zeros
+        const uint32_t idesc = (uint32_t)uniform(
+            (int)idesc_of(p.fp16, MODE != kFwd, MODE == kWgrad, kPair,
+                          MODE == kWgrad ? kPair : (uint32_t)((t.rows + 15) & ~15)));
+        if (!warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma, false)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kPair);
+        for (int k = 0; k < nk; ++k) {
+          // WGRAD: the other CTA's cleaned rows come with its arrival
+          if (!warp_wait(&full[stage], phase, kFlagMma, MODE == kWgrad)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          d = tmem_base + (uint32_t)(acc * kPair);
-        }
-        for (int k = 0; k < t.nk; ++k) {
-          uint8_t* s_a = smem + stage * kStageBytes;
-          int k16 = kK / 16;
-          if (MODE == kWgrad) {
-            const int rem = t.kcnt - k * kK;  // rows of the segment in this step
-            if (rem < kK) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&tail[stage], (tail_phase >> stage) & 1u,
-                                                     abort_flag, p.status, kFlagMma));
-              if (!ok) break;
-              tail_phase ^= 1u << stage;
-              k16 = (rem + 15) / 16;
-              const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
-              uint4* base = reinterpret_cast<uint4*>(s_a);
-              for (int i = lane; i < dirty * 8 * 4; i += 32) {
-                const int box = i / (dirty * 8), j = i - box * dirty * 8;
-                base[box * (kBox / 16) + rem * 8 + j] = make_uint4(0, 0, 0, 0);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&full[stage]), 0));
-            }
+          const uint64_t da = desc_a + (uint64_t)(stage * (kStageBytes >> 4));
+          const uint64_t db = desc_b + (uint64_t)(stage * (kStageBytes >> 4));
+          const int k16 = MODE == kWgrad ? min(kK / 16, (t.kcnt - k * kK + 15) / 16) : kK / 16;
+          if (one) {
+#pragma unroll
+            for (int q = 0; q < kK / 16; ++q)
+              if (MODE != kWgrad || q < k16)
+                umma_bf16_pair(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != 0);
+            umma_commit_pair(&empty[stage], 0x3);
           }
-          if (leader) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.status,
-                                                   kFlagMma, 1000000000ull, MODE == kWgrad));
-            if (!ok) break;
-            if (lane == 0) {
-              tc_fence_after();
-              const uint32_t sa = smem_addr(s_a), sb = sa + kABytes;
-              const uint64_t da = MODE == kFwd ? smem_desc_k_sw128(sa) : smem_desc_mn_sw128(sa);
-              const uint64_t db = MODE == kWgrad ? smem_desc_mn_sw128(sb) : smem_desc_k_sw128(sb);
-              constexpr uint32_t kStepA = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
-              constexpr uint32_t kStepB = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
-              for (int q = 0; q < k16; ++q)
-                umma_bf16_pair(d, da + kStepA * q, db + kStepB * q, idesc, k | q);
-              umma_commit_pair(&empty[stage], 0x3);
-            }
-            __syncwarp();
-          }
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (leader) {
-          if (lane == 0) umma_commit_pair(&tfull[acc], 0x3);
-          __syncwarp();
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
-        }
+        if (one) umma_commit_pair(&tfull[acc], 0x3);
+        __syncwarp();
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      if (leader && lane == 0) {
-        // Every MMA of the pair completes before TMEM is released.
+      // Every MMA of the pair completes before TMEM is released.
+      if (one) {
         umma_commit_pair(drain, 0x1);
         mbar_wait(drain, 0, nullptr, nullptr, 0u, 100000000ull);
       }
     }
     __syncwarp();
+  } else if (MODE == kWgrad && warp == 6) {
+    // ---------------------------------------------------------------- cleaner
+    int stage = 0;
+    uint32_t phase = 0;  // a bit per stage: its tail barrier is used now and then
+    for (;;) {
+      const int ti = read_tile(kFlagProducer);
+      if (ti < 0) break;
+      const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
+      stage = (stage + t.nk) % kStages;
+      const int rem = t.kcnt % kK;  // rows of the segment in its last step
+      if (rem == 0) continue;
+      const int at = stage == 0 ? kStages - 1 : stage - 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tail[at], (phase >> at) & 1u, abort_flag, p.status,
+                                             kFlagProducer)))
+        break;
+      phase ^= 1u << at;
+      const int dirty = (16 - rem % 16) % 16;  // other rows inside the last MMA
+      uint4* base = reinterpret_cast<uint4*>(smem + at * kStageBytes);
+      for (int i = lane; i < dirty * 8 * 4; i += 32) {
+        const int box = i / (dirty * 8), j = i - box * dirty * 8;
+        base[box * (kBox / 16) + rem * 8 + j] = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&full[at]), 0));
+    }
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quadrant of this warp
@@ -463,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     int staged = 0;  // WGRAD: the staging block in turn
     for (;;) {
-      const int ti = read_tile(kFlagEpilogue, true);
+      const int ti = read_tile(kFlagEpilogue);
       if (ti < 0) break;
       const PairTile t = decode_pair<MODE>(ti, p, seg, m_step);
       const bool none = t.nk == 0;
@@ -596,7 +640,7 @@ cudaError_t run_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(PairMem<MODE>::kBlock);
   cfg.dynamicSmemBytes = PairMem<MODE>::kBytes;
   cfg.stream = st;
   cfg.attrs = attr;
