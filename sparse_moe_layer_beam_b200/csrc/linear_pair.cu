@@ -38,7 +38,7 @@ using namespace lin;
 
 constexpr int kThreads = 192;   // WGRAD: a warp more, see below
 constexpr int kPair = 256;     // M and (most) N of a pair's tile
-constexpr int kGroup = 16;     // row blocks that share a sweep over the weights
+constexpr int kGroup = 8;      // row blocks that share a sweep over the weights
 constexpr int kTileSlots = 8;  // tile indices between the fetching producer and the rest
 constexpr int kABytes = 128 * kK * 2;
 constexpr int kBBytes = 128 * kK * 2;
@@ -112,11 +112,11 @@ struct PairTile {
   bool once;       // the weight tile is read by this tile alone
 };
 
-// FWD, DGRAD: the row blocks of all experts, in order, go in groups of 16;
+// FWD, DGRAD: the row blocks of all experts, in order, go in groups of 8;
 // inside a group weight tile by weight tile, row blocks fastest. The pairs at
 // work at one time then share row blocks and weight tiles through L2, and
 // experts with few rows (bound by their weights' bytes) run beside experts
-// with many (bound by the tensor cores). WGRAD: expert by expert, groups of 16
+// with many (bound by the tensor cores). WGRAD: expert by expert, groups of 8
 // column tiles, row tile by row tile.
 template <int MODE>
 __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const Segments& s,
