@@ -42,15 +42,17 @@ struct LinCfg {
   static constexpr int kABytes = kM * kK * 2;
   static constexpr int kBBytes = BN * kK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // persistent: all of shared memory; split: two CTAs per SM
-  static constexpr int kStages = SPLIT ? 4 : (192 * 1024) / kStageBytes;
+  // persistent: all of shared memory; split: two CTAs per SM, and as many
+  // stages (at most 10) as its rows' operand leaves room for
+  static constexpr int kRing = SPLIT ? 96 * 1024 : 192 * 1024 / kStageBytes * kStageBytes;
+  static constexpr int kStages = SPLIT ? 10 : kRing / kStageBytes;
   static constexpr int kAccStages = SPLIT ? 1 : 2;
   static constexpr int kTmemCols = kAccStages * BN;  // 64, 256 or 512
   static constexpr int kBarBytes = 256;
   static constexpr int kTabBytes = 4 * (3 * kMaxE + 16);
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kTabBytes;
+  static constexpr int kSmemBytes = 1024 + kRing + kBarBytes + kTabBytes;
   static_assert(kSmemBytes <= 232448, "dynamic shared memory above the sm_100 limit");
-  static_assert(!SPLIT || kStages * kStageBytes >= kM * BN * 4, "partial tile in the ring");
+  static_assert(!SPLIT || kRing >= kM * BN * 4, "partial tile in the ring");
 };
 
 struct Tile {
@@ -161,22 +163,26 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const LinParams p) {
   using C = LinCfg<BN, SPLIT>;
-  constexpr int STAGES = C::kStages;
+  // Split: with few rows the stages of A lie closer together than the 128
+  // rows an MMA reads of them; what follows fills lanes that are not stored.
+  const int STAGES = SPLIT ? p.stages : C::kStages;
+  const int a_stage = SPLIT ? p.a_stage : C::kABytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  uint8_t* ring_b = smem + STAGES * a_stage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* tab = reinterpret_cast<int*>(smem + STAGES * C::kStageBytes + C::kBarBytes);
+  int* tab = reinterpret_cast<int*>(smem + C::kRing + C::kBarBytes);
   const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
   int* scratch = tab + 3 * kMaxE + 1;  // a word per warp
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
   uint32_t parts = 1;
   if (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_base = (uint32_t)uniform((int)*tmem_holder);
   const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
   const int bn_out = glu ? BN / 2 : BN;
   const int total = MODE == kWgrad ? p.E * p.m_blk * p.n_blk : seg.rb[p.E] * p.n_blk;
@@ -211,74 +217,86 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   const int step = SPLIT ? total : gridDim.x;  // split: one tile per cluster
   // this CTA's contraction steps of a tile
   auto k_range = [&](const Tile& t, int& ka, int& kb) {
-    ka = SPLIT ? (int)((int64_t)t.nk * rank / parts) : 0;
-    kb = SPLIT ? (int)((int64_t)t.nk * (rank + 1) / parts) : t.nk;
+    ka = SPLIT ? uniform((int)((int64_t)t.nk * rank / parts)) : 0;
+    kb = SPLIT ? uniform((int)((int64_t)t.nk * (rank + 1) / parts)) : uniform(t.nk);
+  };
+  // A wait of the whole warp.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity, uint32_t flag) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, flag));
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------ TMA producer
-      const uint64_t pol_stream = policy_evict_first();
-      const uint64_t pol_keep = policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int ti = first; ti < total && ok; ti += step) {
-        const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
-        int ka, kb;
-        k_range(t, ka, kb);
-        const int boxes_a = MODE == kWgrad ? 2 : (t.rows + p.box_a - 1) / p.box_a;
-        const uint32_t bytes_a = MODE == kWgrad ? C::kABytes : boxes_a * p.box_a * kK * 2;
-        const uint64_t pol_w = t.once ? pol_stream : pol_keep;
-        for (int k = ka; k < kb; ++k) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kFlagProducer)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * C::kStageBytes;
-          uint8_t* sb = sa + C::kABytes;
-          mbar_arrive_expect_tx(&full[stage], bytes_a + C::kBBytes);
+    // -------------------------------------------------------- TMA producer
+    const uint64_t pol_stream = policy_evict_first();
+    const uint64_t pol_keep = policy_evict_normal();
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int ti = first; ti < total && ok; ti += step) {
+      const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
+      int ka, kb;
+      k_range(t, ka, kb);
+      const int boxes_a = MODE == kWgrad ? 2 : (t.rows + p.box_a - 1) / p.box_a;
+      const uint32_t box_bytes = p.box_a * kK * 2;
+      const uint32_t tx = (MODE == kWgrad ? C::kABytes : boxes_a * box_bytes) + C::kBBytes;
+      const uint64_t pol_w = t.once ? pol_stream : pol_keep;
+      for (int k = ka; k < kb; ++k) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, kFlagProducer)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * a_stage;
+        uint8_t* sb = ring_b + stage * C::kBBytes;
+        uint64_t* bar = &full[stage];
+        const int kx = k * kK;
+        if (one) {
+          mbar_arrive_expect_tx(bar, tx);
           if (MODE == kWgrad) {
-            const int r = t.k0 + k * kK;
+#pragma unroll
             for (int b = 0; b < 2; ++b)
-              tma_load_2d(sa + b * kBox, &tm_a, &full[stage], t.row0 + b * 64, r, pol_keep);
+              tma_load_2d(sa + b * kBox, &tm_a, bar, t.row0 + b * 64, t.k0 + kx, pol_keep);
 #pragma unroll
             for (int b = 0; b < BN / 64; ++b)
-              tma_load_2d(sb + b * kBox, &tm_b, &full[stage], t.n0 + b * 64, r, pol_keep);
+              tma_load_2d(sb + b * kBox, &tm_b, bar, t.n0 + b * 64, t.k0 + kx, pol_keep);
           } else {
-            for (int b = 0; b < boxes_a; ++b)
-              tma_load_2d(sa + b * p.box_a * kK * 2, &tm_a, &full[stage], k * kK,
-                          t.row0 + b * p.box_a, pol_keep);
             if (MODE == kFwd) {
-              tma_load_3d(sb, &tm_b, &full[stage], k * kK, t.n0, t.e, pol_w);
+              tma_load_3d(sb, &tm_b, bar, kx, t.n0, t.e, pol_w);
               if (glu)
-                tma_load_3d(sb + C::kBBytes / 2, &tm_b, &full[stage], k * kK, p.n_out + t.n0, t.e,
-                            pol_w);
+                tma_load_3d(sb + C::kBBytes / 2, &tm_b, bar, kx, p.n_out + t.n0, t.e, pol_w);
             } else {
 #pragma unroll
               for (int b = 0; b < BN / 64; ++b)
-                tma_load_3d(sb + b * kBox, &tm_b, &full[stage], t.n0 + b * 64, k * kK, t.e, pol_w);
+                tma_load_3d(sb + b * kBox, &tm_b, bar, t.n0 + b * 64, kx, t.e, pol_w);
             }
-          }
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            for (int b = 0; b < boxes_a; ++b)
+              tma_load_2d(sa + b * box_bytes, &tm_a, bar, kx, t.row0 + b * p.box_a, pol_keep);
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // Let every copy this thread issued land before the CTA can exit.
-      const int64_t from = issued > STAGES ? issued - STAGES : 0;
-      for (int64_t i = from; i < issued; ++i)
+    }
+    // Let every copy this warp issued land before the CTA can exit.
+    if (one)
+      for (int64_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
         mbar_wait(&full[i % STAGES], (uint32_t)((i / STAGES) & 1), nullptr, nullptr, 0u,
                   100000000ull);
-    }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    // The whole warp walks the tiles (it zeroes the rows behind a segment in
-    // WGRAD together); lane 0 issues.
+    // (in WGRAD the warp zeroes the rows behind a segment, too)
+    const bool one = elect_one();
+    const uint32_t sa = smem_addr(smem), sb = smem_addr(ring_b);
+    const uint64_t desc_a = MODE == kWgrad ? smem_desc_mn_sw128(sa) : smem_desc_k_sw128(sa);
+    const uint64_t desc_b = MODE == kFwd ? smem_desc_k_sw128(sb) : smem_desc_mn_sw128(sb);
+    constexpr uint32_t kStepA = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
+    constexpr uint32_t kStepB = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
     int stage = 0;
     uint32_t phase = 0;
     int acc = 0;
@@ -291,41 +309,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
       k_range(t, ka, kb);
       if (ka == kb) continue;  // nothing to add: the epilogue takes zeros
       if (!SPLIT) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status,
-                                               kFlagMma));
+        ok = warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma);
         if (!ok) break;
         tc_fence_after();
       }
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
       for (int k = ka; k < kb; ++k) {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&full[stage], phase, abort_flag, p.status, kFlagMma));
+        ok = warp_wait(&full[stage], phase, kFlagMma);
         if (!ok) break;
-        const uint32_t sa = smem_addr(smem + stage * C::kStageBytes);
-        const uint32_t sb = sa + C::kABytes;
         int k16 = kK / 16;
         if (MODE == kWgrad) {
           const int rem = t.kcnt - k * kK;  // rows of the segment in this step
           if (rem < kK) {
             k16 = (rem + 15) / 16;
             const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
-            uint4* base = reinterpret_cast<uint4*>(smem + stage * C::kStageBytes);
             for (int i = lane; i < dirty * 8 * (2 + BN / 64); i += 32) {
               const int box = i / (dirty * 8), j = i - box * dirty * 8;
-              base[box * (kBox / 16) + rem * 8 + j] = make_uint4(0, 0, 0, 0);
+              uint8_t* base = box < 2 ? smem + stage * a_stage + box * kBox
+                                      : ring_b + stage * C::kBBytes + (box - 2) * kBox;
+              reinterpret_cast<uint4*>(base)[rem * 8 + j] = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
         }
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t da = MODE == kWgrad ? smem_desc_mn_sw128(sa) : smem_desc_k_sw128(sa);
-          const uint64_t db = MODE == kFwd ? smem_desc_k_sw128(sb) : smem_desc_mn_sw128(sb);
-          constexpr uint32_t kStepA = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
-          constexpr uint32_t kStepB = MODE == kFwd ? 32 >> 4 : 2048 >> 4;
-          for (int q = 0; q < k16; ++q)
-            umma_bf16(d, da + kStepA * q, db + kStepB * q, idesc, (k - ka) | q);
+        tc_fence_after();
+        const uint64_t da = desc_a + (uint64_t)(stage * (a_stage >> 4));
+        const uint64_t db = desc_b + (uint64_t)(stage * (C::kBBytes >> 4));
+        if (one) {
+#pragma unroll
+          for (int q = 0; q < kK / 16; ++q)
+            if (MODE != kWgrad || q < k16)
+              umma_bf16(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != ka);
           umma_commit(&empty[stage]);
         }
         __syncwarp();
@@ -335,15 +350,15 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
         }
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(&tfull[acc]);
+      if (one) umma_commit(&tfull[acc]);
       __syncwarp();
       if (!SPLIT) {
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
     }
-    if (lane == 0) {
-      // Every MMA this thread issued completes before TMEM is released.
+    if (one) {
+      // Every MMA this warp issued completes before TMEM is released.
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, nullptr, 0u, 100000000ull);
     }
@@ -417,20 +432,35 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
       }
     }
     cluster_sync();
-    if (warp >= 2 && have && r < t.rows) {
+    if (warp >= 2 && have) {
+      // a thread per row and 4 columns; the loads of all parts go out together
       const int per = bn_out / (int)parts;  // 4 at least
-      const uint32_t mine = smem_addr(part) + 4u * r;
-      for (int c0 = rank * per; c0 < (int)(rank + 1) * per; c0 += 4) {
+      for (int i = threadIdx.x - 64; i < t.rows * (per / 4); i += 128) {
+        const int g = i / t.rows, row = i - g * t.rows;
+        const int c0 = rank * per + 4 * g;
+        const uint32_t mine = smem_addr(part) + 4u * (kM * c0 + row);
         float a[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t s = 0; s < parts; ++s) {
+        float va[8][4], vu[8][4];
+#pragma unroll
+        for (uint32_t s = 0; s < 8; ++s) {
+          if (s >= parts) break;
           const uint32_t from = mapa_shared(mine, s);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            a[j] += ld_dsmem_f32(from + 4u * kM * (c0 + j));
-            if (glu) u[j] += ld_dsmem_f32(from + 4u * kM * (BN / 2 + c0 + j));
+            va[s][j] = ld_dsmem_f32(from + 4u * kM * j);
+            vu[s][j] = glu ? ld_dsmem_f32(from + 4u * kM * (BN / 2 + j)) : 0.0f;
           }
         }
-        finish4<MODE>(p, t, r, t.n0 + c0, a, u);
+#pragma unroll
+        for (uint32_t s = 0; s < 8; ++s) {
+          if (s >= parts) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] += va[s][j];
+            u[j] += vu[s][j];
+          }
+        }
+        finish4<MODE>(p, t, row, t.n0 + c0, a, u);
       }
     }
     cluster_sync();  // no CTA leaves while another reads its part
@@ -638,6 +668,15 @@ cudaError_t launch_product(const LinParams& base, const void* a, const void* b, 
   // few bytes; 8 .. 128
   p.box_a = 8;
   while (p.box_a < 128 && p.box_a < 2 * R / E) p.box_a *= 2;
+
+  // split: stages of A hold the rows of the largest possible tile
+  p.a_stage = LinCfg<64, true>::kABytes;
+  if (MODE != kWgrad && R <= 32) {
+    p.box_a = R <= 8 ? 8 : R <= 16 ? 16 : 32;
+    p.a_stage = p.box_a * kK * 2;
+  }
+  p.stages = LinCfg<64, true>::kRing / (p.a_stage + LinCfg<64, true>::kBBytes);
+  if (p.stages > LinCfg<64, true>::kStages) p.stages = LinCfg<64, true>::kStages;
 
   CUtensorMap ta, tb;
   cudaError_t err;

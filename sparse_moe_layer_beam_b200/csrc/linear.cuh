@@ -28,6 +28,7 @@ struct LinParams {
   int nk;                  // contraction steps (FWD, DGRAD)
   int n_blk, m_blk;        // column tiles; row tiles of dW_e (WGRAD)
   int box_a;               // rows per box of the row operand (FWD, DGRAD)
+  int a_stage, stages;     // split: bytes of the row operand per stage, stages
   int act, fp16, out32;
   const float* bias;       // [E][n_w] or NULL
   const void* residual;    // [rows][n_out] or NULL
@@ -110,6 +111,20 @@ __device__ __forceinline__ int find_expert(const int* rb, int E, int q) {
   }
   return a;
 }
+
+// One lane of a converged warp, in the form the compiler knows to be one: the
+// loops around it stay uniform, so that descriptors and addresses live in
+// uniform registers. Issued from inside an `if (lane == 0)` each MMA cost the
+// thread some 70 cycles of register moves, and a step more than its MMAs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // -------------------------------------------------------------- descriptors
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,

@@ -87,20 +87,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
-// One lane of a converged warp, in the form the compiler knows to be one: the
-// loops around it stay uniform, so that descriptors and addresses live in
-// uniform registers. Issued from inside an `if (lane == 0)` each MMA cost the
-// thread some 70 cycles of register moves, and a step more than its MMAs.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 // -------------------------------------------------------------------- tiles
 struct PairTile {
   int e;
