@@ -381,47 +381,47 @@ class Trace:
 
 # ------------------------------------------------------ row and linear operators
 
+# These calls can be shorter on the GPU than on the host, so the checks are kept
+# to one comparison each and what torch is asked for is asked once a call.
+
 _NAMES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
-_types = None
-
-
-def _torch_types():
-    """Tensor types accepted for each dtype (bf16 also as its 16-bit pattern)."""
-    global _types
-    if _types is None:
-        import torch
-        _types = ((torch.bfloat16, torch.int16, torch.uint16), (torch.float16,),
-                  (torch.float32,), (torch.int32,))
-    return _types
-
-
 _I32 = 3
+_types = None    # tensor types of each kind (bf16 also as its 16-bit pattern)
+_device = None   # () -> current CUDA device
+_raw_stream = None  # (device) -> its current stream
 
 
-def _tensor(name, t, kind, *shape):
-    """Address of a contiguous tensor of this type and shape on the current
-    CUDA device; None passes."""
+def _bind_torch():
+    global _types, _device, _raw_stream
+    import torch
+    _types = ((torch.bfloat16, torch.int16, torch.uint16), (torch.float16,),
+              (torch.float32,), (torch.int32,))
+    _device = torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _begin(name, t):
+    """The current device, which tensor t (never None) has to be on."""
+    if t is None:
+        raise ValueError(f"{name}: a tensor is required")
+    if _types is None:
+        _bind_torch()
+    if not t.is_cuda or t.get_device() != _device():
+        raise ValueError(f"{name}: not on the current CUDA device")
+    return t.get_device()
+
+
+def _tensor(name, t, kind, dev, *shape):
+    """Address of a contiguous tensor of this kind and shape on device dev;
+    None passes."""
     if t is None:
         return None
-    if t.dtype not in (_types or _torch_types())[kind]:
-        raise ValueError(f"{name}: unexpected type {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    return _on_device(name, t)
-
-
-def _on_device(name, t):
-    d = t.get_device()
-    if d < 0 or d != _current_device():
-        raise ValueError(f"{name}: not on the current CUDA device")
-    return t.data_ptr()
-
-
-def _current_device():
-    import torch
-    return torch.cuda.current_device()
+    if (t.shape == shape and t.dtype in _types[kind] and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}; "
+                     f"expected a contiguous {_types[kind][0]} {shape} on cuda:{dev}")
 
 
 def _need(name, t):
@@ -430,9 +430,15 @@ def _need(name, t):
     return t
 
 
-def _bytes(ws):
-    """(address, bytes) of a workspace."""
-    return _on_device("ws", _need("ws", ws)), ws.numel() * ws.element_size()
+def _workspace(ws, dev):
+    """(address, bytes) of a workspace on device dev."""
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is required")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _on(dev, stream):
+    return _raw_stream(dev) if stream is None else stream
 
 
 def rows_cfg(width, n_experts, top_k, dtype="bf16"):
@@ -451,57 +457,57 @@ def beam_moe_permute_workspace_size(cfg, T):
 def beam_moe_permute(cfg, x, topk_ids, xp, pos, offsets, ws, stream=None):
     """Token rows sorted by expert: x [T, H], topk_ids [T, K] int32 -> xp
     [T*K, H], pos [T, K] int32, offsets [E+1] int32."""
-    T, K = _need("x", x).shape[0], cfg.top_k
-    d = cfg.dtype
-    args = (_tensor("x", x, d, T, cfg.width),
-            _tensor("topk_ids", _need("topk_ids", topk_ids), _I32, T, K),
-            _tensor("xp", _need("xp", xp), d, T * K, cfg.width),
-            _tensor("pos", _need("pos", pos), _I32, T, K),
-            _tensor("offsets", _need("offsets", offsets), _I32, cfg.n_experts + 1))
-    _check(lib().beam_moe_permute(ctypes.byref(cfg), T, *args, *_bytes(ws), _stream(stream)),
-           "beam_moe_permute")
+    dev = _begin("x", x)
+    T, H, K, d = x.shape[0], cfg.width, cfg.top_k, cfg.dtype
+    _check(lib().beam_moe_permute(
+        cfg, T, _tensor("x", x, d, dev, T, H),
+        _tensor("topk_ids", _need("topk_ids", topk_ids), _I32, dev, T, K),
+        _tensor("xp", _need("xp", xp), d, dev, T * K, H),
+        _tensor("pos", _need("pos", pos), _I32, dev, T, K),
+        _tensor("offsets", _need("offsets", offsets), _I32, dev, cfg.n_experts + 1),
+        *_workspace(ws, dev), _on(dev, stream)), "beam_moe_permute")
 
 
 def beam_moe_permute_backward(cfg, dxp, pos, dx, stream=None):
     """dx[t] = sum_k dxp[pos[t, k]]: dxp [rows, H], pos [T, K] -> dx [T, H]."""
-    T, rows = _need("dx", dx).shape[0], _need("dxp", dxp).shape[0]
-    args = (_tensor("dxp", dxp, cfg.dtype, rows, cfg.width),
-            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
-            _tensor("dx", dx, cfg.dtype, T, cfg.width))
-    _check(lib().beam_moe_permute_backward(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
-           "beam_moe_permute_backward")
+    dev = _begin("dx", dx)
+    T, rows, H, d = dx.shape[0], _need("dxp", dxp).shape[0], cfg.width, cfg.dtype
+    _check(lib().beam_moe_permute_backward(
+        cfg, T, rows, _tensor("dxp", dxp, d, dev, rows, H),
+        _tensor("pos", _need("pos", pos), _I32, dev, T, cfg.top_k),
+        _tensor("dx", dx, d, dev, T, H), _on(dev, stream)), "beam_moe_permute_backward")
 
 
 def _y_kind(cfg, y):
     """FP32 for fp32 rows, else the configuration's dtype."""
-    return FP32 if y.dtype == (_types or _torch_types())[FP32][0] else cfg.dtype
+    return FP32 if y.dtype is _types[FP32][0] else cfg.dtype
 
 
 def beam_moe_combine(cfg, y, pos, w, out, stream=None):
     """out[t] = sum_k w[t, k] y[pos[t, k]]: y [rows, H] of cfg's dtype or fp32,
     w [T, K] fp32 or None (ones) -> out [T, H]."""
-    T, rows = _need("out", out).shape[0], _need("y", y).shape[0]
+    dev = _begin("out", out)
+    T, rows, H, K = out.shape[0], _need("y", y).shape[0], cfg.width, cfg.top_k
     kind = _y_kind(cfg, y)
-    args = (_tensor("y", y, kind, rows, cfg.width), kind,
-            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
-            _tensor("w", w, FP32, T, cfg.top_k), _tensor("out", out, cfg.dtype, T, cfg.width))
-    _check(lib().beam_moe_combine(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
-           "beam_moe_combine")
+    _check(lib().beam_moe_combine(
+        cfg, T, rows, _tensor("y", y, kind, dev, rows, H), kind,
+        _tensor("pos", _need("pos", pos), _I32, dev, T, K), _tensor("w", w, FP32, dev, T, K),
+        _tensor("out", out, cfg.dtype, dev, T, H), _on(dev, stream)), "beam_moe_combine")
 
 
 def beam_moe_combine_backward(cfg, dout, y, pos, w, dy, dw, stream=None):
     """dy[pos[t, k]] = w[t, k] dout[t] (dy as y, or None), dw[t, k] =
     <dout[t], y[pos[t, k]]> (fp32 [T, K], or None; y may be None without it)."""
-    T = _need("dout", dout).shape[0]
+    dev = _begin("dout", dout)
     like = y if y is not None else _need("dy", dy)
-    rows, kind = like.shape[0], _y_kind(cfg, like)
-    args = (_tensor("dout", dout, cfg.dtype, T, cfg.width),
-            _tensor("y", y, kind, rows, cfg.width), kind,
-            _tensor("pos", _need("pos", pos), _I32, T, cfg.top_k),
-            _tensor("w", w, FP32, T, cfg.top_k), _tensor("dy", dy, kind, rows, cfg.width),
-            _tensor("dw", dw, FP32, T, cfg.top_k))
-    _check(lib().beam_moe_combine_backward(ctypes.byref(cfg), T, rows, *args, _stream(stream)),
-           "beam_moe_combine_backward")
+    T, rows, H, K = dout.shape[0], like.shape[0], cfg.width, cfg.top_k
+    kind = _y_kind(cfg, like)
+    _check(lib().beam_moe_combine_backward(
+        cfg, T, rows, _tensor("dout", dout, cfg.dtype, dev, T, H),
+        _tensor("y", y, kind, dev, rows, H), kind,
+        _tensor("pos", _need("pos", pos), _I32, dev, T, K), _tensor("w", w, FP32, dev, T, K),
+        _tensor("dy", dy, kind, dev, rows, H), _tensor("dw", dw, FP32, dev, T, K),
+        _on(dev, stream)), "beam_moe_combine_backward")
 
 
 def linear_cfg(n_in, n_out, n_experts=1, act="none", dtype="bf16", out_fp32=False):
@@ -512,7 +518,7 @@ def linear_cfg(n_in, n_out, n_experts=1, act="none", dtype="bf16", out_fp32=Fals
 
 
 def _weight_rows(cfg):
-    return cfg.n_out * 2 if ACTS[cfg.act] == "swiglu" else cfg.n_out
+    return cfg.n_out * 2 if cfg.act == 5 else cfg.n_out
 
 
 def beam_moe_linear_workspace_size(cfg, rows, backward=False):
@@ -529,28 +535,31 @@ def beam_moe_linear(cfg, x, w, y, ws, bias=None, residual=None, offsets=None, z=
     [rows, n_in], w [E, N, n_in] (N = n_out, 2 n_out for swiglu), bias [E, N]
     fp32, residual [rows, n_out], offsets [E+1] int32 (None: one expert) -> y
     [rows, n_out] and, if given, z [rows, N] = x w_e^T + bias_e."""
-    rows, E, N, d = _need("x", x).shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
-    out = FP32 if cfg.out_fp32 else d
-    args = (_tensor("x", x, d, rows, cfg.n_in), _tensor("w", _need("w", w), d, E, N, cfg.n_in),
-            _tensor("bias", bias, FP32, E, N),
-            _tensor("residual", residual, out, rows, cfg.n_out),
-            _tensor("offsets", offsets, _I32, E + 1),
-            _tensor("y", _need("y", y), out, rows, cfg.n_out), _tensor("z", z, d, rows, N))
-    _check(lib().beam_moe_linear(ctypes.byref(cfg), rows, *args, *_bytes(ws), _stream(stream)),
-           "beam_moe_linear")
+    dev = _begin("x", x)
+    rows, E, N, d = x.shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
+    K, M, out = cfg.n_in, cfg.n_out, FP32 if cfg.out_fp32 else d
+    _check(lib().beam_moe_linear(
+        cfg, rows, _tensor("x", x, d, dev, rows, K),
+        _tensor("w", _need("w", w), d, dev, E, N, K), _tensor("bias", bias, FP32, dev, E, N),
+        _tensor("residual", residual, out, dev, rows, M),
+        _tensor("offsets", offsets, _I32, dev, E + 1),
+        _tensor("y", _need("y", y), out, dev, rows, M), _tensor("z", z, d, dev, rows, N),
+        *_workspace(ws, dev), _on(dev, stream)), "beam_moe_linear")
 
 
 def beam_moe_linear_backward(cfg, dy, x, w, ws, dx=None, dw=None, dbias=None, z=None,
                              offsets=None, stream=None):
     """Gradients of beam_moe_linear: dy [rows, n_out], x, w and the forward's z
     -> dx [rows, n_in], dw [E, N, n_in], dbias [E, N] fp32 (each may be None)."""
-    rows, E, N, d = _need("dy", dy).shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
-    args = (_tensor("dy", dy, d, rows, cfg.n_out), _tensor("x", x, d, rows, cfg.n_in),
-            _tensor("w", w, d, E, N, cfg.n_in), _tensor("z", z, d, rows, N),
-            _tensor("offsets", offsets, _I32, E + 1), _tensor("dx", dx, d, rows, cfg.n_in),
-            _tensor("dw", dw, d, E, N, cfg.n_in), _tensor("dbias", dbias, FP32, E, N))
-    _check(lib().beam_moe_linear_backward(ctypes.byref(cfg), rows, *args, *_bytes(ws),
-                                          _stream(stream)), "beam_moe_linear_backward")
+    dev = _begin("dy", dy)
+    rows, E, N, d = dy.shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
+    K, M = cfg.n_in, cfg.n_out
+    _check(lib().beam_moe_linear_backward(
+        cfg, rows, _tensor("dy", dy, d, dev, rows, M), _tensor("x", x, d, dev, rows, K),
+        _tensor("w", w, d, dev, E, N, K), _tensor("z", z, d, dev, rows, N),
+        _tensor("offsets", offsets, _I32, dev, E + 1), _tensor("dx", dx, d, dev, rows, K),
+        _tensor("dw", dw, d, dev, E, N, K), _tensor("dbias", dbias, FP32, dev, E, N),
+        *_workspace(ws, dev), _on(dev, stream)), "beam_moe_linear_backward")
 
 
 # ------------------------------------------------------------ expert parallelism

@@ -143,45 +143,58 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int* total) {
 }
 
 // offsets, and cnt turned from counts into the first row of (chunk, expert).
-// One CTA: thread (j, e) sums the j-th part of expert e's chunks.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t* __restrict__ cnt, int nchunks,
+// A CTA turns 16 experts' columns; each reads all counts once for the totals
+// (128 KB from L2 at 131072 assignments to 256 experts: 3 us, where one CTA for
+// everything took 10).
+constexpr int kScanExperts = 16;
+
+__global__ void __launch_bounds__(1024) sort_scan_kernel(const int32_t* __restrict__ cnt,
+                                                         int32_t* __restrict__ base, int nchunks,
                                                          int E, int32_t* __restrict__ offsets) {
   __shared__ int part[1024];
+  __shared__ int s_off[kMaxE];
   __shared__ int warp_tot[32], total;
   const int tid = threadIdx.x;
-  const int per_e = 1024 / E;  // E <= 512
-  const int e = tid % E, j = tid / E;
-  const int len = (nchunks + per_e - 1) / per_e;
-  const int c0 = min(nchunks, j * len), c1 = min(nchunks, c0 + len);
-  const bool act = j < per_e;
-  int sum = 0;
-  if (act)
+  {
+    // thread (j, e) sums the j-th part of expert e's chunks
+    const int per_e = 1024 / E;  // E <= 512
+    const int e = tid % E, j = tid / E;
+    const int len = (nchunks + per_e - 1) / per_e;
+    const int c0 = min(nchunks, j * len), c1 = min(nchunks, c0 + len);
+    int sum = 0;
+    if (j < per_e)
 #pragma unroll 8
-    for (int c = c0; c < c1; ++c) sum += cnt[(size_t)c * E + e];
+      for (int c = c0; c < c1; ++c) sum += __ldg(cnt + (size_t)c * E + e);
+    part[tid] = sum;
+    __syncthreads();
+    int tot = 0;
+    if (tid < E)
+      for (int q = 0; q < per_e; ++q) tot += part[q * E + tid];
+    const int off = block_scan(tid < E ? tot : 0, warp_tot, &total);
+    if (tid < E) s_off[tid] = off;
+    if (blockIdx.x == 0) {
+      if (tid < E) offsets[tid] = off;
+      if (tid == 0) offsets[E] = total;
+    }
+    __syncthreads();
+  }
+  // thread (j, e) turns the j-th of 64 parts of one of this CTA's experts
+  const int e = blockIdx.x * kScanExperts + tid % kScanExperts, j = tid / kScanExperts;
+  const int len = (nchunks + 63) / 64;
+  const int c0 = min(nchunks, j * len), c1 = min(nchunks, c0 + len);
+  int sum = 0;
+  if (e < E)
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) sum += __ldg(cnt + (size_t)c * E + e);
   part[tid] = sum;
   __syncthreads();
-  int tot = 0;
-  if (tid < E)
-    for (int q = 0; q < per_e; ++q) tot += part[q * E + tid];
-  const int off = block_scan(tid < E ? tot : 0, warp_tot, &total);
-  if (tid < E) offsets[tid] = off;
-  if (tid == 0) offsets[E] = total;
-  __syncthreads();
-  if (tid < E) {  // part becomes the first row of (part, expert)
-    int run = off;
-    for (int q = 0; q < per_e; ++q) {
-      const int c = part[q * E + tid];
-      part[q * E + tid] = run;
-      run += c;
-    }
-  }
-  __syncthreads();
-  if (act) {
-    int run = part[tid];
-#pragma unroll 8
+  if (e < E) {
+    int run = s_off[e];
+    for (int q = 0; q < j; ++q) run += part[q * kScanExperts + tid % kScanExperts];
+#pragma unroll 4
     for (int c = c0; c < c1; ++c) {
-      const int v = cnt[(size_t)c * E + e];
-      cnt[(size_t)c * E + e] = run;
+      const int v = __ldg(cnt + (size_t)c * E + e);
+      base[(size_t)c * E + e] = run;
       run += v;
     }
   }
@@ -192,7 +205,7 @@ constexpr int kCopyThreads = 256;
 // Copies x[t] to its rows for `tpb` tokens per CTA, a slice of the row per
 // blockIdx.y. V: the unit of the copy (16, 4 or 2 bytes; nv of them per row).
 // ONE: the positions are counted here, from all ids (A <= kOneLaunch).
-template <class V, bool ONE>
+template <class V, bool ONE, int U>
 __global__ void __launch_bounds__(kCopyThreads)
     permute_rows_kernel(const V* __restrict__ x, int nv, int64_t T, int K, int E, int tpb,
                         const int32_t* __restrict__ ids, const uint16_t* __restrict__ rank,
@@ -256,14 +269,22 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
   }
   __syncthreads();
+  // U units per thread and pass, loaded together
   const int step = gridDim.y * kCopyThreads;
   for (int i = 0; i < nt; ++i) {
     const V* src = x + (t0 + i) * nv;
-    for (int v = blockIdx.y * kCopyThreads + tid; v < nv; v += step) {
-      const V d = __ldg(src + v);
+    for (int v = blockIdx.y * kCopyThreads + tid; v < nv; v += U * step) {
+      V d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v + u * step < nv) d[u] = __ldg(src + v + u * step);
       for (int k = 0; k < K; ++k) {
         const int p = s_pos[i * K + k];
-        if (p >= 0) xp[(size_t)p * nv + v] = d;
+        if (p < 0) continue;
+        V* dst = xp + (size_t)p * nv + v;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v + u * step < nv) dst[u * step] = d[u];
       }
     }
   }
@@ -273,8 +294,11 @@ __global__ void __launch_bounds__(kCopyThreads)
 constexpr int kRowThreads = 128;
 
 // out[t] = sum_k w[t,k] y[pos[t,k]] (w NULL: 1). A CTA per token and slice of
-// the row; N elements per thread and step.
-template <class O, class Y, int N>
+// the row; U packs of N elements per thread and pass, the loads of eight slots
+// in flight at once (four, where packs are single elements). 4096 tokens x
+// 5120 bf16 x 8 slots: 61 us, 5.75 TB/s; FP32 rows 106 us, 6.7 TB/s. (A warp
+// per piece of a row, walking pieces without barriers: 65 to 87 us.)
+template <class O, class Y, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
     combine_rows_kernel(const Y* __restrict__ y, int H, int K, int64_t rows,
                         const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -289,80 +313,131 @@ __global__ void __launch_bounds__(kRowThreads)
     s_w[tid] = w ? w[t * K + tid] : 1.0f;
   }
   __syncthreads();
-  const int nv = H / N;
-  for (int v = blockIdx.y * kRowThreads + tid; v < nv; v += gridDim.y * kRowThreads) {
-    float acc[N];
+  const int nv = H / N, step = gridDim.y * kRowThreads;
+  for (int v = blockIdx.y * kRowThreads + tid; v < nv; v += U * step) {
+    float acc[U][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-#pragma unroll 4
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[u][i] = 0.0f;
+#pragma unroll(N == 8 ? 8 : 4)
     for (int k = 0; k < K; ++k) {
       const int p = s_pos[k];
       if (p < 0) continue;
-      const Pack<Y, N> r = load_pack<Y, N>(y + (size_t)p * H + (size_t)v * N);
+      const Y* row = y + (size_t)p * H + (size_t)v * N;
       const float wk = s_w[k];
+      Pack<Y, N> r[U];
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = fmaf(wk, to_f32(r.v[i]), acc[i]);
+      for (int u = 0; u < U; ++u)
+        if (v + u * step < nv) r[u] = load_pack<Y, N>(row + (size_t)u * step * N);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[u][i] = fmaf(wk, to_f32(r[u].v[i]), acc[u][i]);
     }
-    Pack<O, N> o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<O>(acc[i]);
-    store_pack<O, N>(out + (size_t)t * H + (size_t)v * N, o);
+    for (int u = 0; u < U; ++u) {
+      if (v + u * step >= nv) break;
+      Pack<O, N> o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.v[i] = from_f32<O>(acc[u][i]);
+      store_pack<O, N>(out + (size_t)t * H + (size_t)(v + u * step) * N, o);
+    }
   }
 }
 
-// dy rows and dw of one token's slots k = blockIdx.y, blockIdx.y + gridDim.y,
-// ... A thread's products are added in column order, a warp's by a shuffle
-// tree, the four warps' in order: the sum has one order whatever runs when.
-template <class O, class Y, int N>
-__global__ void __launch_bounds__(kRowThreads)
+// dy rows and dw of one token's slots, S of them at a time (groups of S from
+// blockIdx.y on, gridDim.y groups apart), U packs of N elements per thread and
+// pass. A thread's products are added in column order, a warp's by a shuffle
+// tree, the warps' in order: the sum has one order whatever runs when.
+// 4096 tokens x 5120 bf16 x 8 slots: 122 us, 5.85 TB/s (one slot at a time 145
+// us, four 136 us, 256 threads 129 us; FP32 rows want 256 threads).
+template <class O, class Y, int N, int S, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     combine_bwd_kernel(const O* __restrict__ dout, const Y* __restrict__ y, int H, int K,
                        int64_t rows, const int32_t* __restrict__ pos,
                        const float* __restrict__ w, Y* __restrict__ dy, float* __restrict__ dw) {
-  __shared__ float s_sum[kMaxK][kRowThreads / 32];
+  __shared__ float s_sum[kMaxK + S][THREADS / 32];
+  __shared__ int s_pos[kMaxK + S];
+  __shared__ float s_w[kMaxK + S];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
+  if (tid < kMaxK + S) {
+    const int p = tid < K ? pos[t * K + tid] : -1;
+    s_pos[tid] = p < rows ? p : -1;
+    s_w[tid] = w && tid < K ? w[t * K + tid] : 1.0f;
+  }
+  __syncthreads();
   const int nv = H / N;
   const O* d = dout + (size_t)t * H;
-  for (int k = blockIdx.y; k < K; k += gridDim.y) {
-    int p = pos[t * K + k];
-    if (p >= rows) p = -1;
-    float sum = 0.0f;
-    if (p >= 0) {
-      const float wk = w ? w[t * K + k] : 1.0f;
-#pragma unroll 4
-      for (int v = tid; v < nv; v += kRowThreads) {
-        const Pack<O, N> g = load_pack<O, N>(d + (size_t)v * N);
-        const size_t at = (size_t)p * H + (size_t)v * N;
+  for (int k = S * blockIdx.y; k < K; k += S * gridDim.y) {
+    int p[S];
+    float wk[S], sum[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      p[j] = s_pos[k + j];
+      wk[j] = s_w[k + j];
+      sum[j] = 0.0f;
+    }
+    for (int v = tid; v < nv; v += U * THREADS) {
+      Pack<Y, N> r[S][U];
+      Pack<O, N> g[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const size_t off = (size_t)(v + u * THREADS) * N;
+        if (v + u * THREADS >= nv) break;
         if (dw) {
-          const Pack<Y, N> r = load_pack<Y, N>(y + at);
 #pragma unroll
-          for (int i = 0; i < N; ++i) sum = fmaf(to_f32(g.v[i]), to_f32(r.v[i]), sum);
+          for (int j = 0; j < S; ++j)
+            if (p[j] >= 0) r[j][u] = load_pack<Y, N>(y + (size_t)p[j] * H + off);
         }
-        if (dy) {
-          Pack<Y, N> o;
+        g[u] = load_pack<O, N>(d + off);
+      }
 #pragma unroll
-          for (int i = 0; i < N; ++i) o.v[i] = from_f32<Y>(wk * to_f32(g.v[i]));
-          store_pack<Y, N>(dy + at, o);
+      for (int u = 0; u < U; ++u) {
+        const size_t off = (size_t)(v + u * THREADS) * N;
+        if (v + u * THREADS >= nv) break;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          if (p[j] < 0) continue;
+          if (dw) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              sum[j] = fmaf(to_f32(g[u].v[i]), to_f32(r[j][u].v[i]), sum[j]);
+          }
+          if (dy) {
+            Pack<Y, N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) o.v[i] = from_f32<Y>(wk[j] * to_f32(g[u].v[i]));
+            store_pack<Y, N>(dy + (size_t)p[j] * H + off, o);
+          }
         }
       }
     }
     if (dw) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if ((tid & 31) == 0) s_sum[k][tid >> 5] = sum;
+      for (int j = 0; j < S; ++j) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if ((tid & 31) == 0) s_sum[k + j][tid >> 5] = sum[j];
+      }
     }
   }
   if (dw) {
     __syncthreads();
-    for (int k = blockIdx.y + tid * gridDim.y; k < K; k += kRowThreads * gridDim.y)
-      dw[t * K + k] = (s_sum[k][0] + s_sum[k][1]) + (s_sum[k][2] + s_sum[k][3]);
+    if (tid < K && tid / S % gridDim.y == blockIdx.y) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < THREADS / 32; ++i) sum += s_sum[tid][i];
+      dw[t * K + tid] = sum;
+    }
   }
 }
 
 // ------------------------------------------------------------------- launches
 struct SortLayout {
   int nchunks;
-  size_t rank, cnt, total;
+  size_t rank, cnt, base, total;
 };
 
 SortLayout sort_layout(const beam_moe_rows_cfg& c, int64_t T) {
@@ -372,7 +447,9 @@ SortLayout sort_layout(const beam_moe_rows_cfg& c, int64_t T) {
   L.rank = 256;
   const size_t rank_bytes = ((size_t)A * 2 + 255) / 256 * 256;
   L.cnt = L.rank + rank_bytes;
-  L.total = A <= kOneLaunch ? 256 : L.cnt + ((size_t)L.nchunks * c.n_experts * 4 + 255) / 256 * 256;
+  const size_t cnt_bytes = ((size_t)L.nchunks * c.n_experts * 4 + 255) / 256 * 256;
+  L.base = L.cnt + cnt_bytes;
+  L.total = A <= kOneLaunch ? 256 : L.base + cnt_bytes;
   return L;
 }
 
@@ -384,12 +461,17 @@ cudaError_t run_permute(const beam_moe_rows_cfg& c, int64_t T, const void* x, co
   const int64_t A = T * K;
   const int nv = (int)((size_t)c.width * dtype_bytes(c.dtype) / sizeof(V));
   const bool one = A <= kOneLaunch;
-  // about four CTAs per SM, at most 8 tokens (and 256 assignments) each; with
-  // few tokens a row is cut into slices instead
+  // Positions at hand: a CTA per token (16384 tokens x 5120 to 8 experts each:
+  // 257 us; 2, 8 and 16 tokens per CTA: 264, 278 and 302 us). Counted by every
+  // CTA: about four CTAs per SM, at most 8 tokens (and 256 assignments) each.
+  // With few tokens a row is cut into slices besides.
   const int64_t want = 4 * (int64_t)device_sm_count();
-  int tpb = (int)(T / want < 1 ? 1 : T / want);
-  if (tpb > 8) tpb = 8;
-  if (tpb * K > kCopyThreads) tpb = kCopyThreads / K;
+  int tpb = 1;
+  if (one) {
+    tpb = (int)(T / want < 1 ? 1 : T / want);
+    if (tpb > 8) tpb = 8;
+    if (tpb * K > kCopyThreads) tpb = kCopyThreads / K;
+  }
   const int64_t gx = (T + tpb - 1) / tpb;
   int64_t gy = (want / 2 + gx - 1) / gx;
   const int most = (nv + kCopyThreads - 1) / kCopyThreads;
@@ -398,21 +480,24 @@ cudaError_t run_permute(const beam_moe_rows_cfg& c, int64_t T, const void* x, co
   const dim3 grid((unsigned)gx, (unsigned)gy);
   const V* xv = static_cast<const V*>(x);
   V* xpv = static_cast<V*>(xp);
+  constexpr int U = sizeof(V) == 16 ? 1 : 4;
   if (one) {
-    permute_rows_kernel<V, true><<<grid, kCopyThreads, 0, st>>>(xv, nv, T, K, E, tpb, ids, nullptr,
-                                                                nullptr, pos, offsets, xpv);
+    permute_rows_kernel<V, true, U><<<grid, kCopyThreads, 0, st>>>(
+        xv, nv, T, K, E, tpb, ids, nullptr, nullptr, pos, offsets, xpv);
     return cudaGetLastError();
   }
   uint16_t* rank = reinterpret_cast<uint16_t*>(ws + L.rank);
   int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* base = reinterpret_cast<int32_t*>(ws + L.base);
   sort_count_kernel<<<L.nchunks, kSortChunk, 0, st>>>(ids, A, E, rank, cnt);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  sort_scan_kernel<<<1, 1024, 0, st>>>(cnt, L.nchunks, E, offsets);
+  sort_scan_kernel<<<(E + kScanExperts - 1) / kScanExperts, 1024, 0, st>>>(cnt, base, L.nchunks, E,
+                                                                           offsets);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  permute_rows_kernel<V, false><<<grid, kCopyThreads, 0, st>>>(xv, nv, T, K, E, tpb, ids, rank, cnt,
-                                                               pos, offsets, xpv);
+  permute_rows_kernel<V, false, U><<<grid, kCopyThreads, 0, st>>>(xv, nv, T, K, E, tpb, ids, rank,
+                                                                  base, pos, offsets, xpv);
   return cudaGetLastError();
 }
 
@@ -423,11 +508,17 @@ cudaError_t run_combine(const beam_moe_rows_cfg& c, int64_t T, int64_t rows, con
   const Y* yy = static_cast<const Y*>(y);
   O* oo = static_cast<O*>(out);
   if (H % 8 == 0) {
-    const dim3 grid((unsigned)T, (unsigned)h_slices(T, H / 8));
-    combine_rows_kernel<O, Y, 8><<<grid, kRowThreads, 0, st>>>(yy, H, K, rows, pos, w, oo);
+    // one pass per thread, however many tokens (4096 tokens: 61 us; all five
+    // passes of a row in one CTA 64 us)
+    const dim3 grid((unsigned)T, (unsigned)((H / 8 + kRowThreads - 1) / kRowThreads));
+    combine_rows_kernel<O, Y, 8, 1><<<grid, kRowThreads, 0, st>>>(yy, H, K, rows, pos, w, oo);
   } else {
-    const dim3 grid((unsigned)T, (unsigned)h_slices(T, H));
-    combine_rows_kernel<O, Y, 1><<<grid, kRowThreads, 0, st>>>(yy, H, K, rows, pos, w, oo);
+    // enough CTAs for eight per SM (4000 tokens x 1003: one CTA per token 11.6
+    // us, one pass per thread 13.3 us)
+    const int64_t want = (8 * (int64_t)device_sm_count() + T - 1) / T;
+    const int64_t most = (H + 4 * kRowThreads - 1) / (4 * kRowThreads);
+    const dim3 grid((unsigned)T, (unsigned)(want < most ? want : most));
+    combine_rows_kernel<O, Y, 1, 4><<<grid, kRowThreads, 0, st>>>(yy, H, K, rows, pos, w, oo);
   }
   return cudaGetLastError();
 }
@@ -437,16 +528,20 @@ cudaError_t run_combine_bwd(const beam_moe_rows_cfg& c, int64_t T, int64_t rows,
                             const void* y, const int32_t* pos, const float* w, void* dy, float* dw,
                             cudaStream_t st) {
   const int H = c.width, K = c.top_k;
-  int64_t gy = (4 * (int64_t)device_sm_count() + T - 1) / T;  // few tokens: their slots apart
-  if (gy > K) gy = K;
-  const dim3 grid((unsigned)T, (unsigned)gy);
   const O* d = static_cast<const O*>(dout);
   const Y* yy = static_cast<const Y*>(y);
   Y* o = static_cast<Y*>(dy);
-  if (H % 8 == 0)
-    combine_bwd_kernel<O, Y, 8><<<grid, kRowThreads, 0, st>>>(d, yy, H, K, rows, pos, w, o, dw);
+  const int S = H % 8 == 0 ? 2 : 1;
+  int64_t gy = (8 * (int64_t)device_sm_count() + T - 1) / T;  // few tokens: their slots apart
+  if (gy > (K + S - 1) / S) gy = (K + S - 1) / S;
+  const dim3 grid((unsigned)T, (unsigned)gy);
+  constexpr int kThreads = sizeof(Y) == 2 ? 128 : 256;
+  if (S == 2)
+    combine_bwd_kernel<O, Y, 8, 2, 1, kThreads>
+        <<<grid, kThreads, 0, st>>>(d, yy, H, K, rows, pos, w, o, dw);
   else
-    combine_bwd_kernel<O, Y, 1><<<grid, kRowThreads, 0, st>>>(d, yy, H, K, rows, pos, w, o, dw);
+    combine_bwd_kernel<O, Y, 1, 1, 8, 128>
+        <<<grid, 128, 0, st>>>(d, yy, H, K, rows, pos, w, o, dw);
   return cudaGetLastError();
 }
 
