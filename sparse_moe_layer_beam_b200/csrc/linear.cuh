@@ -35,8 +35,18 @@ struct LinParams {
   void* z;                 // [rows][n_w] or NULL
   void* out;
   unsigned* status;
+  int clear_status;        // the launch clears the status area (the first of a call)
   int* next_tile;          // CTA pairs: counter of the tiles handed out
 };
+
+constexpr int kStatusWords = 64;
+
+// The status word and the counters of a call, by one CTA of its first launch.
+// (The launches after it find them clear; a wait of this launch that gives up
+// sets its bit a second from now.)
+__device__ __forceinline__ void clear_status_area(const LinParams& p) {
+  if (threadIdx.x < kStatusWords) p.status[threadIdx.x] = 0;
+}
 
 // ------------------------------------------------------------- the segments
 // Segment of expert e, clamped into the rows there are whatever offsets holds.
