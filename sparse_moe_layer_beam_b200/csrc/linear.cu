@@ -49,10 +49,10 @@ struct LinCfg {
   static constexpr int kAccStages = SPLIT ? 1 : 2;
   static constexpr int kTmemCols = kAccStages * BN;  // 64, 256 or 512
   static constexpr int kBarBytes = 256;
-  static constexpr int kTabBytes = 4 * (3 * kMaxE + 16);
+  static constexpr int kTabBytes = 4 * (3 * kMaxE + 12 + 64);  // and 64 biases (split)
   static constexpr int kSmemBytes = 1024 + kRing + kBarBytes + kTabBytes;
   static_assert(kSmemBytes <= 232448, "dynamic shared memory above the sm_100 limit");
-  static_assert(!SPLIT || kRing >= kM * BN * 4, "partial tile in the ring");
+  static_assert(!SPLIT || kRing >= (kM + 1) * BN * 4, "partial tile in the ring");
 };
 
 struct Tile {
@@ -107,21 +107,22 @@ __device__ __forceinline__ Tile decode(int t, const LinParams& p, const Segments
   return d;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Four columns n .. n + 3 of one row of D: a (and, for swiglu, the up values
-// u). n_out and n_in are multiples of 8, so four columns exist together.
+// u). n_out and n_in are multiples of 8, so four columns exist together. bias:
+// that of column n, and of its up value `up` floats further.
 template <int MODE>
 __device__ __forceinline__ void finish4(const LinParams& p, const Tile& t, int r, int n, float* a,
-                                        float* u) {
+                                        float* u, const float* bias, int up) {
   if (n >= p.cols) return;
   if (MODE == kWgrad) {
     store4(p.out, ((int64_t)t.e * p.n_w + t.row0 + r) * p.n_in + n, a, false, p.fp16);
@@ -134,11 +135,10 @@ __device__ __forceinline__ void finish4(const LinParams& p, const Tile& t, int r
   }
   const bool glu = p.act == BEAM_MOE_ACT_SWIGLU;
   if (p.bias) {
-    const float* b = p.bias + (int64_t)t.e * p.n_w + n;
-    const float4 f = __ldg(reinterpret_cast<const float4*>(b));
+    const float4 f = *reinterpret_cast<const float4*>(bias);
     a[0] += f.x; a[1] += f.y; a[2] += f.z; a[3] += f.w;
     if (glu) {
-      const float4 g = __ldg(reinterpret_cast<const float4*>(b + p.n_out));
+      const float4 g = *reinterpret_cast<const float4*>(bias + up);
       u[0] += g.x; u[1] += g.y; u[2] += g.z; u[3] += g.w;
     }
   }
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* tab = reinterpret_cast<int*>(smem + C::kRing + C::kBarBytes);
   const Segments seg = {tab, tab + kMaxE, tab + 2 * kMaxE};
-  int* scratch = tab + 3 * kMaxE + 1;  // a word per warp
+  int* scratch = tab + 3 * kMaxE + 4;  // a word per warp, then 64 biases
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
           float* fa = reinterpret_cast<float*>(a);
           float* fu = reinterpret_cast<float*>(u);
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) finish4<MODE>(p, t, r, t.n0 + c0 + j, fa + j, fu + j);
+          for (int j = 0; j < 16; j += 4)
+            finish4<MODE>(p, t, r, t.n0 + c0 + j, fa + j, fu + j,
+                          p.bias + (int64_t)t.e * p.n_w + t.n0 + c0 + j, p.n_out);
         }
       }
       if (!none) {
@@ -418,32 +420,33 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   }
 
   if (SPLIT) {
-    // Each CTA leaves its partial sums in its own shared memory, column by
-    // column (the ring is free: its MMAs are done), and finishes bn_out/parts
-    // columns, adding the parts in CTA order.
+    // Each CTA leaves its partial sums in its own shared memory (the ring is
+    // free: its MMAs are done) and finishes bn_out / parts columns, reading
+    // the other parts of them and adding all in CTA order. (Storing them into
+    // the finishing CTA instead takes a second barrier before: 1.5 us more.)
     const int q = warp & 3, r = q * 32 + lane;
+    constexpr int kLd = kM + 1;  // rows of a column, one off: no bank conflicts below
     float* part = reinterpret_cast<float*>(smem);
+    float* s_bias = reinterpret_cast<float*>(scratch + 8);
     const bool have = first < total;
+    const int per = bn_out / (int)parts;  // 4 at least
     Tile t;
     if (have) t = decode<MODE, BN>(first, p, seg, bn_out);
     if (warp >= 2 && have) {
       if (MODE == kFwd) {  // what the epilogue reads, on its way before the sums are there
-        const int per = bn_out / (int)parts, n = t.n0 + rank * per;
-        const int row = threadIdx.x - 64;
-        if (row < t.rows && n < p.cols) {
-          if (p.residual)
-            prefetch_l2(static_cast<const uint8_t*>(p.residual) +
-                        ((int64_t)(t.row0 + row) * p.n_out + n) * (p.out32 ? 4 : 2));
-          if (p.bias && row == 0) {
-            prefetch_l2(p.bias + (int64_t)t.e * p.n_w + n);
-            if (glu) prefetch_l2(p.bias + (int64_t)t.e * p.n_w + p.n_out + n);
-          }
+        const int n = t.n0 + rank * per, i = threadIdx.x - 64;
+        if (p.residual && i < t.rows && n < p.cols)
+          prefetch_l2(static_cast<const uint8_t*>(p.residual) +
+                      ((int64_t)(t.row0 + i) * p.n_out + n) * (p.out32 ? 4 : 2));
+        if (p.bias && i < (glu ? 2 : 1) * per) {
+          const int c = n + (i < per ? i : i - per);
+          if (c < p.cols)
+            s_bias[i] = __ldg(p.bias + (int64_t)t.e * p.n_w + (i < per ? 0 : p.n_out) + c);
         }
       }
       int ka, kb;
       k_range(t, ka, kb);
-      const bool got = ka < kb && __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, abort_flag,
-                                                                   p.status, kFlagEpilogue));
+      const bool got = ka < kb && warp_wait(&tfull[0], 0, kFlagEpilogue);
       tc_fence_after();
       for (int c0 = 0; c0 < BN; c0 += 16) {
         uint32_t a[16];
@@ -454,17 +457,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c0 + j) * kM + r] = __uint_as_float(a[j]);
+        for (int j = 0; j < 16; ++j) part[(c0 + j) * kLd + r] = __uint_as_float(a[j]);
       }
     }
     cluster_sync();
     if (warp >= 2 && have) {
-      // a thread per row and 4 columns; the loads of all parts go out together
-      const int per = bn_out / (int)parts;  // 4 at least
+      // a thread per row and 4 columns, columns fastest; the loads of all
+      // parts go out together
       for (int i = threadIdx.x - 64; i < t.rows * (per / 4); i += 128) {
-        const int g = i / t.rows, row = i - g * t.rows;
-        const int c0 = rank * per + 4 * g;
-        const uint32_t mine = smem_addr(part) + 4u * (kM * c0 + row);
+        const int row = i / (per / 4), c = 4 * (i - row * (per / 4));
+        const uint32_t mine = smem_addr(part + ((int)rank * per + c) * kLd + row);
         float a[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
         float va[8][4], vu[8][4];
 #pragma unroll
@@ -473,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
           const uint32_t from = mapa_shared(mine, s);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            va[s][j] = ld_dsmem_f32(from + 4u * kM * j);
-            vu[s][j] = glu ? ld_dsmem_f32(from + 4u * kM * (BN / 2 + j)) : 0.0f;
+            va[s][j] = ld_dsmem_f32(from + 4u * kLd * j);
+            vu[s][j] = glu ? ld_dsmem_f32(from + 4u * kLd * (BN / 2 + j)) : 0.0f;
           }
         }
 #pragma unroll
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
             u[j] += vu[s][j];
           }
         }
-        finish4<MODE>(p, t, row, t.n0 + c0, a, u);
+        finish4<MODE>(p, t, row, t.n0 + (int)rank * per + c, a, u, s_bias + c, per);
       }
     }
     cluster_sync();  // no CTA leaves while another reads its part
@@ -706,50 +708,90 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Lin
   return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BN, SPLIT>, ta, tb, p);
 }
 
-// The product of one mode. Column tiles of 256 while those make a tile for
-// every SM, else of 128, else of 64 with the contraction split over a cluster
-// (at least 4 steps a CTA).
+// How a product runs: which tile, and on how many CTAs each.
+struct Choice {
+  int bn;     // columns per tile; 0: CTA pairs
+  int parts;  // CTAs that split a tile's contraction (bn = 64)
+};
+
+// The four forms by their estimated times, in microseconds: a fixed part and a
+// part per contraction step for each turn a CTA takes. The steps' costs are
+// measured (16 shapes from 64 x 5120 x 5120 to 16000 x 640 x 640, each form
+// forced): a step of 128 x 64, 128 x 128 and 128 x 256 on one CTA 0.37, 0.27
+// and 0.48, of 256 x 256 on a pair 0.40. What the estimate decides, for one
+// expert and 5120 x 5120: 64 rows split 22.7 (pairs 24.7), 256 rows 128
+// columns 28.0 (split 33.4, pairs 37.8), 500 rows pairs 39.8 (128 columns
+// 48.0), 800 rows 256 columns 46.3 (pairs 62.7, two turns for 6 of 74), 1500
+// rows pairs 64 (256 columns 78). dW on pairs wins whenever they have a tile
+// each (64 x 5120 x 5120: 26.8 against 53.1), its stores go out by TMA.
+Choice choose(int mode, const LinParams& p, bool glu) {
+  const double R = p.rows, E = p.E, sms = device_sm_count();
+  auto up = [](double a, double b) { return (double)(int64_t)((a + b - 1) / b); };
+  // turns of `slots` workers over t tiles, which are not all full
+  auto turns = [](double t, double slots) {
+    const double w = t / slots;
+    return w <= 1.0 ? 1.0 : 0.5 * (w + (double)(int64_t)(w + 0.999999));
+  };
+  // row blocks of X: the full ones and the experts' last ones, half of which
+  // are taken to be there
+  auto row_blocks = [&](double m) { return up(R, m) + (E < R ? E - 1 : R - 1) / 2; };
+  const bool dw = mode == kWgrad;
+  const double steps = dw ? up(R / E, kK) : up(mode == kFwd ? p.n_in : p.n_w, kK);
+  auto tiles = [&](double m, double n) {
+    return dw ? E * up(p.n_w, m) * up(p.n_in, n) : row_blocks(m) * up(p.cols, glu ? n / 2 : n);
+  };
+  Choice best = {64, 1};
+  const double t64 = tiles(128, 64);
+  // Clusters of up to 1.5 CTAs per SM are resident at once. Each part has two
+  // steps at least, four where there are many rows to join (300 x 520 x 1320,
+  // dW: 9.4 us against 11.4; one row, 1000 x 520: 6.0 with two, 7.0 with four).
+  const double least_steps = !dw && R / E <= 32 ? 2 : 4;
+  while (best.parts < 8 && t64 * best.parts * 2 <= 1.5 * sms &&
+         steps >= 2 * least_steps * best.parts)
+    best.parts *= 2;
+  double least = turns(t64 * best.parts, 2 * sms) * (steps / best.parts * 0.37 + 6.0);
+  auto consider = [&](int bn, double us) {
+    if (us < least) {
+      least = us;
+      best = {bn, 1};
+    }
+  };
+  const double out = dw ? 3.0 : 0.0;  // dW's stores, which few steps do not hide
+  consider(128, turns(tiles(128, 128), sms) * (steps * 0.27 + out) + 9.0);
+  consider(256, turns(tiles(128, 256), sms) * (steps * 0.48 + 2 * out) + 12.0);
+  // experts with few rows stream their weights: one CTA per tile does that at
+  // the copy bandwidth, a pair at 0.9 of it
+  if (dw || R / E >= 96) {
+    const double t = dw ? tiles(256, 256) : row_blocks(256) * up(p.cols, glu ? 128 : 256);
+    consider(0, turns(t, sms / 2) * (steps * 0.40 + 0.7 * out) + 8.0);
+  }
+  return best;
+}
+
 template <int MODE>
 cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
   LinParams p = base;
   const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
-  const int64_t R = p.rows, E = p.E;
-  const int64_t sms = device_sm_count();
-  // row blocks: at most this many (every expert may end inside one)
-  const int64_t rb = MODE == kWgrad ? E * ((p.n_w + kM - 1) / kM) : R / kM + (E < R ? E : R);
-  const int64_t rb_sure = MODE == kWgrad ? rb : (R + kM - 1) / kM > E / 2 ? (R + kM - 1) / kM
-                                                                          : (E < R ? E : R) / 2;
-  auto blocks = [&](int bn) { return (p.cols + (glu ? bn / 2 : bn) - 1) / (glu ? bn / 2 : bn); };
-  // CTA pairs once they all have a tile and a segment fills a good part of a
-  // 256-row block (WGRAD: of a few steps); below that the products stream
-  // their weights (or dW) and one CTA per tile does that better.
-  const int64_t pair_tiles =
-      MODE == kWgrad ? E * ((p.n_w + 255) / 256) * ((p.n_in + 255) / 256)
-                     : (R + 255) / 256 * (glu ? (p.n_out + 127) / 128 : (p.cols + 255) / 256);
-  if (pair_tiles >= sms / 2 && R / E >= 96) {
+  const Choice c = choose(MODE, p, glu);
+  if (c.bn == 0) {
     if (p.clear_status) {  // the counter has to be zero before the first pair starts
       const cudaError_t e = cudaMemsetAsync(p.status, 0, kStatusWords * 4, st);
       if (e != cudaSuccess) return e;
     }
     return launch_linear_pair(MODE, base, a, b, st);
   }
-  int bn = 64;
-  if (rb_sure * blocks(256) >= sms) bn = 256;
-  else if (rb_sure * blocks(128) >= sms) bn = 128;
-  p.n_blk = blocks(bn);
+  const int bn = c.bn, parts = c.parts;
+  const int64_t R = p.rows, E = p.E;
+  p.n_blk = (p.cols + (glu ? bn / 2 : bn) - 1) / (glu ? bn / 2 : bn);
   p.m_blk = (p.n_w + kM - 1) / kM;
   const int kc = MODE == kFwd ? p.n_in : p.n_w;
   p.nk = (kc + kK - 1) / kK;
-  const int64_t tiles = rb * p.n_blk;
-  const int64_t steps = MODE == kWgrad ? (R / E + kK - 1) / kK : p.nk;
-  int parts = 1;
-  while (bn == 64 && parts < 8 && rb_sure * p.n_blk * parts * 2 <= 2 * sms && steps >= 8 * parts)
-    parts *= 2;
+  // row blocks: at most this many (every expert may end inside one)
+  const int64_t tiles = p.n_blk * (MODE == kWgrad ? E * p.m_blk : R / kM + (E < R ? E : R));
   // boxes of the row operand: about an expert's rows, so that few rows cost
   // few bytes; 8 .. 128
   p.box_a = 8;
   while (p.box_a < 128 && p.box_a < 2 * R / E) p.box_a *= 2;
-
   // split: stages of A hold the rows of the largest possible tile
   p.a_stage = LinCfg<64, true>::kABytes;
   if (MODE != kWgrad && R <= 32) {
