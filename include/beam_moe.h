@@ -546,7 +546,7 @@ typedef enum beam_moe_act {
 } beam_moe_act;
 
 /* Supported: n_in and n_out multiples of 8 up to 65536, n_experts 1..512,
- * dtype bf16 or fp16, up to 2^30 rows. */
+ * dtype bf16 or fp16, up to 2^26 rows. */
 typedef struct beam_moe_linear_cfg {
   int32_t n_in;      /* width of X                                            */
   int32_t n_out;     /* width of Y                                            */

@@ -882,7 +882,8 @@ beam_moe_status check_linear(const beam_moe_linear_cfg* c, int64_t rows) {
   if (c->out_fp32 != 0 && c->out_fp32 != 1) return BEAM_MOE_ERR_INVALID_ARG;
   if (c->n_in % 8 || c->n_out % 8 || c->n_in > 65536 || c->n_out > 65536 || c->n_experts > kMaxE)
     return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
-  if (rows > (int64_t)1 << 30) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
+  // dW sums over the rows inside one bounded wait: 2^26 of them take half its second
+  if (rows > (int64_t)1 << 26) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
   return BEAM_MOE_OK;
 }
 
