@@ -23,9 +23,16 @@
 //  - Enough tiles for the SMs: persistent CTAs, TMA producer, MMA issuer and
 //    four epilogue warps, accumulators double-buffered in TMEM. Fewer: a
 //    cluster of up to 8 CTAs splits the contraction of a tile and joins its
-//    partial sums through distributed shared memory, in CTA order.
+//    partial sums through distributed shared memory, in CTA order. Many rows
+//    per expert: CTA pairs (linear_pair.cu). Up to four rows: no tiles at all,
+//    the weights stream through the CUDA cores (linear_few_kernel). choose()
+//    picks the form by estimated time.
+//  - Each role is a whole warp whose loops are uniform, one elected lane issuing
+//    (see elect_one).
 // Every wait is bounded (see sm100.cuh).
 #include <string.h>
+
+#include <type_traits>
 
 #include "linear.cuh"
 #include "ops.h"
@@ -501,6 +508,155 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   }
 }
 
+// ------------------------------------------------------------- a few rows
+constexpr int kFewThreads = 128;
+constexpr int kFewRows = 4;              // rows of X at most
+constexpr int kFewBytes = 40 * 1024;     // of them in shared memory
+
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* v, bool fp16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16(w[i], fp16);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// The forward for up to four rows (decode): the weights stream through the
+// CUDA cores, two weight rows a warp, FP32 FMAs against X in shared memory, the
+// next weights' loads in flight meanwhile; lanes' sums are added by a
+// shuffle tree. RT rows of a dense layer share the weights; with experts
+// (RT = 1) blockIdx.y is the row. Bound by HBM: one token through 5120 x 5120
+// 11.8 us, 4.4 TB/s, a call's fixed part included (tensor cores 17.3 us); four
+// rows of four experts, swiglu, 41 us (58). One weight row a warp with twice
+// the loads 13.3 us, four vectors per turn 14.8.
+template <int RT, bool GLU>
+__global__ void __launch_bounds__(kFewThreads)
+    linear_few_kernel(const LinParams p, const uint16_t* __restrict__ x,
+                      const uint16_t* __restrict__ w) {
+  extern __shared__ uint4 s_x[];  // [RT][n_in / 8]
+  if (p.clear_status && blockIdx.x == 0 && blockIdx.y == 0) clear_status_area(p);
+  const int lane = threadIdx.x & 31;
+  // this warp's weight rows: the gate and up rows of column n, or columns n
+  // and n + 1 (n_out is even)
+  const int slot = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
+  const int slots = GLU ? p.n_out : p.n_out / 2;
+  const bool live = slot < slots;
+  const int n = (GLU ? 1 : 2) * min(slot, slots - 1);
+  const int row0 = RT == 1 ? blockIdx.y : 0;
+  int e = 0;
+  if (p.offsets) {  // the first expert whose segment holds the row
+    e = -1;
+    for (int e0 = 0; e0 < p.E && e < 0; e0 += 32) {
+      int lo = 0, cnt = 0;
+      if (e0 + lane < p.E) segment(p, e0 + lane, lo, cnt);
+      const unsigned hit = __ballot_sync(0xffffffffu, row0 >= lo && row0 < lo + cnt);
+      if (hit) e = e0 + __ffs(hit) - 1;
+    }
+    if (e < 0) return;  // behind the last expert's rows
+  }
+  const bool fp16 = p.fp16;
+  const int nv = p.n_in / 8;  // 16-byte vectors of a row
+  const uint16_t* wr = w + ((int64_t)e * p.n_w + n) * p.n_in;
+  const int64_t second = GLU ? (int64_t)p.n_out * p.n_in : p.n_in;
+  constexpr int U = 2;  // vectors of each row per lane and turn
+  uint4 g[2][U], u[2][U];
+  auto fetch = [&](int b, int v0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = v0 + 32 * i;
+      if (v < nv) {
+        g[b][i] = load_once(wr + 8 * v);
+        u[b][i] = load_once(wr + second + 8 * v);
+      }
+    }
+  };
+  fetch(0, lane);
+  const uint4* xr = reinterpret_cast<const uint4*>(x + (int64_t)row0 * p.n_in);
+  const int rows = min(RT, p.rows - row0);
+  for (int i = threadIdx.x; i < RT * nv; i += kFewThreads)
+    s_x[i] = i < rows * nv ? __ldg(xr + i) : make_uint4(0, 0, 0, 0);
+  // what the end needs, on its way: lane r finishes row r
+  const bool mine = live && lane < rows;
+  const int64_t at = (int64_t)(row0 + lane) * p.n_out + n;
+  float bias[2] = {0.0f, 0.0f}, residual[2] = {0.0f, 0.0f};
+  if (p.bias) {
+    bias[0] = __ldg(p.bias + (int64_t)e * p.n_w + n);
+    bias[1] = __ldg(p.bias + (int64_t)e * p.n_w + n + (GLU ? p.n_out : 1));
+  }
+  if (p.residual && mine) {
+    residual[0] = load1(p.residual, at, p.out32, fp16);
+    if (!GLU) residual[1] = load1(p.residual, at + 1, p.out32, fp16);
+  }
+  __syncthreads();
+
+  float acc[RT], accu[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = accu[r] = 0.0f;
+  auto add = [&](int b, int v0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = v0 + 32 * i;
+      if (v >= nv) break;
+      float wf[8], uf[8];
+      unpack8(g[b][i], wf, fp16);
+      unpack8(u[b][i], uf, fp16);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float xf[8];
+        unpack8(s_x[r * nv + v], xf, fp16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[r] = fmaf(wf[j], xf[j], acc[r]);
+          accu[r] = fmaf(uf[j], xf[j], accu[r]);
+        }
+      }
+    }
+  };
+  constexpr int kTurn = 32 * U;
+  for (int v0 = lane; v0 - lane < nv; v0 += 2 * kTurn) {
+    fetch(1, v0 + kTurn);
+    add(0, v0);
+    fetch(0, v0 + 2 * kTurn);
+    add(1, v0 + kTurn);
+  }
+  float v[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+      accu[r] += __shfl_xor_sync(0xffffffffu, accu[r], o);
+    }
+    if (lane == r) {
+      v[0] = acc[r] + bias[0];
+      v[1] = accu[r] + bias[1];
+    }
+  }
+  if (!mine) return;
+  if (p.z) {
+    const int64_t zt = (int64_t)(row0 + lane) * p.n_w + n;
+    store1(p.z, zt, v[0], false, fp16);
+    store1(p.z, zt + (GLU ? p.n_out : 1), v[1], false, fp16);
+  }
+  if (GLU) {
+    store1(p.out, at, silu_f(v[0]) * v[1] + residual[0], p.out32, fp16);
+  } else {
+    activate<2>(p.act, v);
+    store1(p.out, at, v[0] + residual[0], p.out32, fp16);
+    store1(p.out, at + 1, v[1] + residual[1], p.out32, fp16);
+  }
+}
+
 // ----------------------------------------- dZ and the sums of dZ over rows
 constexpr int kActThreads = 256;
 constexpr int kActPerSm = 4;
@@ -542,16 +698,6 @@ struct ActParams {
   uint16_t* dz;       // NULL: act none
   float* part;        // [row blocks][n_w] or NULL
 };
-
-__device__ __forceinline__ void unpack8(const uint4& u, float* v, bool fp16) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack16(w[i], fp16);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
 
 __device__ __forceinline__ void store8(uint16_t* p, int64_t at, const float* v, bool fp16) {
   *reinterpret_cast<uint4*>(p + at) =
@@ -768,10 +914,44 @@ Choice choose(int mode, const LinParams& p, bool glu) {
   return best;
 }
 
+int few_tile(const LinParams& p) { return p.offsets ? 1 : p.rows <= 1 ? 1 : p.rows <= 2 ? 2 : 4; }
+
+// Three and four rows of a dense layer go there while the weights are small
+// (640 x 640: 3.1 us, tensor cores 6.1); for 5120 x 5120 the rows' FMAs bound
+// it (18.8 us against 16.9).
+bool few_rows(const LinParams& p) {
+  const int rt = few_tile(p);
+  return p.rows <= kFewRows && rt * p.n_in * 2 <= kFewBytes &&
+         (rt <= 2 || (int64_t)p.n_w * p.n_in <= (int64_t)8 << 20);
+}
+
+cudaError_t launch_few(const LinParams& p, const void* x, const void* w, cudaStream_t st) {
+  const bool glu = p.act == BEAM_MOE_ACT_SWIGLU;
+  const int rt = few_tile(p);
+  const int slots = glu ? p.n_out : p.n_out / 2;
+  const dim3 grid((unsigned)((slots + kFewThreads / 32 - 1) / (kFewThreads / 32)),
+                  (unsigned)(p.offsets ? p.rows : 1));
+  const uint16_t* xx = static_cast<const uint16_t*>(x);
+  const uint16_t* ww = static_cast<const uint16_t*>(w);
+  auto run = [&](auto rows, auto gated) {
+    linear_few_kernel<decltype(rows)::value, decltype(gated)::value>
+        <<<grid, kFewThreads, rows.value * p.n_in * 2, st>>>(p, xx, ww);
+    return cudaGetLastError();
+  };
+  using std::integral_constant;
+  auto by_rows = [&](auto gated) {
+    return rt == 1 ? run(integral_constant<int, 1>(), gated)
+                   : rt == 2 ? run(integral_constant<int, 2>(), gated)
+                             : run(integral_constant<int, 4>(), gated);
+  };
+  return glu ? by_rows(std::true_type()) : by_rows(std::false_type());
+}
+
 template <int MODE>
 cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
   LinParams p = base;
   const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
+  if (MODE == kFwd && few_rows(p)) return launch_few(p, a, b, st);
   const Choice c = choose(MODE, p, glu);
   if (c.bn == 0) {
     if (p.clear_status) {  // the counter has to be zero before the first pair starts

@@ -223,6 +223,18 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, bool fp16) {
               : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
+__device__ __forceinline__ float load1(const void* p, int64_t at, bool f32, bool fp16) {
+  if (f32) return static_cast<const float*>(p)[at];
+  return fp16 ? __half2float(static_cast<const __half*>(p)[at])
+              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+
+__device__ __forceinline__ void store1(void* p, int64_t at, float v, bool f32, bool fp16) {
+  if (f32) static_cast<float*>(p)[at] = v;
+  else if (fp16) static_cast<__half*>(p)[at] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
 // 4 consecutive elements at p (element index at, a multiple of 4).
 __device__ __forceinline__ void store4(void* p, int64_t at, const float* v, bool f32, bool fp16) {
   if (f32)

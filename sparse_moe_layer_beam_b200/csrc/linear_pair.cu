@@ -155,12 +155,6 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int4 v) {
                : "memory");
 }
 
-__device__ __forceinline__ float load1(const void* p, int64_t at, bool f32, bool fp16) {
-  if (f32) return static_cast<const float*>(p)[at];
-  return fp16 ? __half2float(static_cast<const __half*>(p)[at])
-              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-
 template <class T>
 __device__ __forceinline__ T narrow(float v);
 template <>
