@@ -168,6 +168,73 @@ __device__ __forceinline__ void finish4(const LinParams& p, const Tile& t, int r
   store4(p.out, row * p.n_out + n, a, p.out32, p.fp16);
 }
 
+// Sixteen columns from n on of one row, as above; eight of them exist together.
+template <int MODE>
+__device__ __forceinline__ void finish16(const LinParams& p, const Tile& t, int r, int n, float* a,
+                                         const float* u) {
+  const int halves = p.cols - n >= 16 ? 2 : 1;
+  if (MODE != kFwd) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    const int64_t at =
+        (MODE == kWgrad ? (int64_t)t.e * p.n_w + t.row0 + r : (int64_t)t.row0 + r) * p.n_in + n;
+    store8(out, at, a, p.fp16);
+    if (halves == 2) store8(out, at + 8, a + 8, p.fp16);
+    return;
+  }
+  const bool glu = p.act == BEAM_MOE_ACT_SWIGLU;
+  const int64_t row = t.row0 + r;
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = glu ? u[j] : 0.0f;
+  if (p.bias) {
+    const float* b = p.bias + (int64_t)t.e * p.n_w + n;
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      if (j >= 8 * halves) break;
+      const float4 f = __ldg(reinterpret_cast<const float4*>(b + j));
+      a[j] += f.x; a[j + 1] += f.y; a[j + 2] += f.z; a[j + 3] += f.w;
+      if (glu) {
+        const float4 g = __ldg(reinterpret_cast<const float4*>(b + p.n_out + j));
+        v[j] += g.x; v[j + 1] += g.y; v[j + 2] += g.z; v[j + 3] += g.w;
+      }
+    }
+  }
+  if (p.z) {
+    uint16_t* z = static_cast<uint16_t*>(p.z);
+    for (int h = 0; h < halves; ++h) {
+      store8(z, row * p.n_w + n + 8 * h, a + 8 * h, p.fp16);
+      if (glu) store8(z, row * p.n_w + p.n_out + n + 8 * h, v + 8 * h, p.fp16);
+    }
+  }
+  if (glu) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] = silu_f(a[j]) * v[j];
+  } else {
+    activate<16>(p.act, a);
+  }
+  const int64_t at = row * p.n_out + n;
+  if (p.residual) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      if (j >= 8 * halves) break;
+      float q[4];
+      load4(p.residual, at + j, q, p.out32, p.fp16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[j + i] += q[i];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; j += 8) {
+    if (j >= 8 * halves) break;
+    if (p.out32) {
+      store4(p.out, at + j, a + j, true, false);
+      store4(p.out, at + j + 4, a + j + 4, true, false);
+    } else {
+      store8(static_cast<uint16_t*>(p.out), at + j, a + j, p.fp16);
+    }
+  }
+}
+
 // ------------------------------------------------------------------- kernel
 template <int MODE, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
@@ -408,14 +475,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
           if (glu) tmem_ld16(tb + BN / 2 + c0, u);
           tmem_ld_wait();
         }
-        if (r < t.rows) {
-          float* fa = reinterpret_cast<float*>(a);
-          float* fu = reinterpret_cast<float*>(u);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            finish4<MODE>(p, t, r, t.n0 + c0 + j, fa + j, fu + j,
-                          p.bias + (int64_t)t.e * p.n_w + t.n0 + c0 + j, p.n_out);
-        }
+        if (r < t.rows)
+          finish16<MODE>(p, t, r, t.n0 + c0, reinterpret_cast<float*>(a),
+                         reinterpret_cast<const float*>(u));
       }
       if (!none) {
         tc_fence_before();
@@ -519,16 +581,6 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float* v, bool fp16) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack16(w[i], fp16);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
 }
 
 // The forward for up to four rows (decode): the weights stream through the
@@ -698,12 +750,6 @@ struct ActParams {
   uint16_t* dz;       // NULL: act none
   float* part;        // [row blocks][n_w] or NULL
 };
-
-__device__ __forceinline__ void store8(uint16_t* p, int64_t at, const float* v, bool fp16) {
-  *reinterpret_cast<uint4*>(p + at) =
-      make_uint4(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16), pack16(v[4], v[5], fp16),
-                 pack16(v[6], v[7], fp16));
-}
 
 // BLOCK rows of one expert x 256 columns at a time, CTAs walking the row
 // blocks: dZ (rounded to 16 bits, the products' operand type) and the block's

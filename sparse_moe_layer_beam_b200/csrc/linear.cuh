@@ -235,6 +235,22 @@ __device__ __forceinline__ void store1(void* p, int64_t at, float v, bool f32, b
   else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void unpack8(const uint4& u, float* v, bool fp16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16(w[i], fp16);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int64_t at, const float* v, bool fp16) {
+  *reinterpret_cast<uint4*>(p + at) =
+      make_uint4(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16), pack16(v[4], v[5], fp16),
+                 pack16(v[6], v[7], fp16));
+}
+
 // 4 consecutive elements at p (element index at, a multiple of 4).
 __device__ __forceinline__ void store4(void* p, int64_t at, const float* v, bool f32, bool fp16) {
   if (f32)
