@@ -236,10 +236,11 @@ __device__ __forceinline__ void finish16(const LinParams& p, const Tile& t, int 
 }
 
 // ------------------------------------------------------------------- kernel
+// bid: this CTA among those of the product. Split: consecutive groups of
+// p.parts CTAs share a tile each (a cluster holds one group or several).
 template <int MODE, int BN, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
-    linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                  const LinParams p) {
+__device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
+                                            const LinParams& p, int bid) {
   using C = LinCfg<BN, SPLIT>;
   // Split: with few rows the stages of A lie closer together than the 128
   // rows an MMA reads of them; what follows fills lanes that are not stored.
@@ -261,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   int* scratch = tab + 3 * kMaxE + 4;  // a word per warp, then 64 biases
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
-  uint32_t parts = 1;
-  if (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+  const uint32_t parts = SPLIT ? p.parts : 1;
+  const uint32_t rank = SPLIT ? cluster_ctarank() & (parts - 1) : 0;  // in its group
+  const uint32_t group0 = SPLIT ? cluster_ctarank() - rank : 0;       // the group's first CTA
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
       seg.rb[1] = (p.rows + kM - 1) / kM;
     }
   }
-  if (p.clear_status && blockIdx.x == 0) clear_status_area(p);
+  if (p.clear_status && bid == 0) clear_status_area(p);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
   const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
   const int bn_out = glu ? BN / 2 : BN;
   const int total = MODE == kWgrad ? p.E * p.m_blk * p.n_blk : seg.rb[p.E] * p.n_blk;
-  const int first = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int first = SPLIT ? bid / (int)parts : bid;
   const int step = SPLIT ? total : gridDim.x;  // split: one tile per cluster
   // this CTA's contraction steps of a tile
   auto k_range = [&](const Tile& t, int& ka, int& kb) {
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
 #pragma unroll
         for (uint32_t s = 0; s < 8; ++s) {
           if (s >= parts) break;
-          const uint32_t from = mapa_shared(mine, s);
+          const uint32_t from = mapa_shared(mine, group0 + s);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             va[s][j] = ld_dsmem_f32(from + 4u * kLd * j);
@@ -568,6 +569,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);
   }
+}
+
+template <int MODE, int BN, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ LinParams p) {
+  linear_body<MODE, BN, SPLIT>(tm_a, tm_b, p, blockIdx.x);
 }
 
 // ------------------------------------------------------------- a few rows
@@ -844,21 +852,22 @@ __global__ void __launch_bounds__(kActThreads, kActPerSm)
   }
 }
 
-// dbias[e] = the sums of e's row blocks, 8 interleaved chains joined in order.
+// dbias[e] = the sums of e's row blocks, 6 interleaved chains joined in order,
+// for 32 columns (block bx) and every by-th expert of n_by.
 template <int BLOCK>
-__global__ void __launch_bounds__(kActThreads)
-    bias_join_kernel(const LinParams p, const float* __restrict__ part, float* __restrict__ dbias) {
+__device__ __forceinline__ void join_bias(const LinParams& p, const float* __restrict__ part,
+                                          float* __restrict__ dbias, int bx, int by, int n_by) {
   __shared__ int tab[kMaxE + 1 + 8];
-  __shared__ float s_sum[8][32];
+  __shared__ float s_sum[kThreads / 32][32];
   const Segments seg = {nullptr, nullptr, tab};
-  build_segments<kActThreads, BLOCK>(p, seg, tab + kMaxE + 1);
+  build_segments<kThreads, BLOCK>(p, seg, tab + kMaxE + 1);
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cl;
-  for (int e = blockIdx.y; e < p.E; e += gridDim.y) {
+  const int c = bx * 32 + cl;
+  for (int e = by; e < p.E; e += n_by) {
     float v = 0.0f;
     if (c < p.n_w)
 #pragma unroll 4
-      for (int q = seg.rb[e] + rl; q < seg.rb[e + 1]; q += 8)
+      for (int q = seg.rb[e] + rl; q < seg.rb[e + 1]; q += kThreads / 32)
         v += __ldg(part + (int64_t)q * p.n_w + c);
     __syncthreads();
     s_sum[rl][cl] = v;
@@ -866,9 +875,43 @@ __global__ void __launch_bounds__(kActThreads)
     if (rl == 0 && c < p.n_w) {
       float t = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) t += s_sum[w][cl];
+      for (int w = 0; w < kThreads / 32; ++w) t += s_sum[w][cl];
       dbias[(int64_t)e * p.n_w + c] = t;
     }
+  }
+}
+
+template <int BLOCK>
+__global__ void __launch_bounds__(kThreads)
+    bias_join_kernel(const LinParams p, const float* __restrict__ part, float* __restrict__ dbias) {
+  join_bias<BLOCK>(p, part, dbias, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// A small backward's products and bias sums in one launch: they only wait for
+// dZ, and each alone leaves SMs idle (39 x 136 x 2872, gelu, dZ included: 14.4 us,
+// in launches of their own 23.4; 1000 x 520 x 1320: 37.0 and 39.8).
+struct Joint {
+  LinParams dx, dw;
+  int dx_ctas, dw_ctas;  // whole clusters each; the CTAs behind them join dbias
+  int join_x, join_y;
+  const float* part;
+  float* dbias;
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+    linear_joint_kernel(const __grid_constant__ CUtensorMap dx_a,
+                        const __grid_constant__ CUtensorMap dx_b,
+                        const __grid_constant__ CUtensorMap dw_a,
+                        const __grid_constant__ CUtensorMap dw_b, const __grid_constant__ Joint j) {
+  const int b = blockIdx.x;
+  if (b < j.dx_ctas) {
+    linear_body<kDgrad, 64, true>(dx_a, dx_b, j.dx, b);
+  } else if (b < j.dx_ctas + j.dw_ctas) {
+    linear_body<kWgrad, 64, true>(dw_a, dw_b, j.dw, b - j.dx_ctas);
+  } else {
+    const int i = b - j.dx_ctas - j.dw_ctas;
+    if (i < j.join_x * j.join_y)
+      join_bias<32>(j.dx, j.part, j.dbias, i % j.join_x, i / j.join_x, j.join_y);
   }
 }
 
@@ -898,6 +941,44 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Lin
   const int64_t sms = device_sm_count();
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * parts : (tiles < sms ? tiles : sms)));
   return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BN, SPLIT>, ta, tb, p);
+}
+
+// dZ and the row blocks' sums of it. CTAs for about eight per SM walk the blocks.
+template <int BLOCK>
+cudaError_t launch_act_blocks(const LinParams& p, const ActParams& a, int64_t blocks,
+                              cudaStream_t st) {
+  const int64_t cols = (p.n_out + kActCols - 1) / kActCols;
+  int64_t gx = (2 * kActPerSm * (int64_t)device_sm_count() + cols - 1) / cols;
+  if (gx > blocks) gx = blocks;
+  const dim3 grid((unsigned)gx, (unsigned)cols);
+  if (p.act == BEAM_MOE_ACT_SWIGLU)
+    act_backward_kernel<BLOCK, true><<<grid, kActThreads, 0, st>>>(p, a);
+  else
+    act_backward_kernel<BLOCK, false><<<grid, kActThreads, 0, st>>>(p, a);
+  return cudaGetLastError();
+}
+
+// CTAs that join dbias: 32 columns and a share of the experts each.
+void join_grid(const LinParams& p, int* x, int* y) {
+  *x = (p.n_w + 31) / 32;
+  const int want = (8 * device_sm_count() + *x - 1) / *x;
+  *y = want < p.E ? want : p.E;
+}
+
+cudaError_t launch_bias_join(const LinParams& p, const float* part, int block, float* dbias,
+                             cudaStream_t st) {
+  int x, y;
+  join_grid(p, &x, &y);
+  const dim3 grid((unsigned)x, (unsigned)y);
+  if (block == 32) bias_join_kernel<32><<<grid, kThreads, 0, st>>>(p, part, dbias);
+  else bias_join_kernel<128><<<grid, kThreads, 0, st>>>(p, part, dbias);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act_backward(const LinParams& p, const ActParams& a, int block, int64_t blocks,
+                                cudaStream_t st) {
+  return block == 32 ? launch_act_blocks<32>(p, a, blocks, st)
+                     : launch_act_blocks<128>(p, a, blocks, st);
 }
 
 // How a product runs: which tile, and on how many CTAs each.
@@ -993,27 +1074,21 @@ cudaError_t launch_few(const LinParams& p, const void* x, const void* w, cudaStr
   return glu ? by_rows(std::true_type()) : by_rows(std::false_type());
 }
 
+// The one-CTA forms' parameters and tensor maps; *tiles: at most so many.
 template <int MODE>
-cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
+cudaError_t set_up(const LinParams& base, const Choice& c, const void* a, const void* b,
+                   LinParams* out, CUtensorMap* ta, CUtensorMap* tb, int64_t* tiles) {
   LinParams p = base;
   const bool glu = MODE == kFwd && p.act == BEAM_MOE_ACT_SWIGLU;
-  if (MODE == kFwd && few_rows(p)) return launch_few(p, a, b, st);
-  const Choice c = choose(MODE, p, glu);
-  if (c.bn == 0) {
-    if (p.clear_status) {  // the counter has to be zero before the first pair starts
-      const cudaError_t e = cudaMemsetAsync(p.status, 0, kStatusWords * 4, st);
-      if (e != cudaSuccess) return e;
-    }
-    return launch_linear_pair(MODE, base, a, b, st);
-  }
-  const int bn = c.bn, parts = c.parts;
+  const int bn = c.bn;
   const int64_t R = p.rows, E = p.E;
+  p.parts = c.parts;
   p.n_blk = (p.cols + (glu ? bn / 2 : bn) - 1) / (glu ? bn / 2 : bn);
   p.m_blk = (p.n_w + kM - 1) / kM;
   const int kc = MODE == kFwd ? p.n_in : p.n_w;
   p.nk = (kc + kK - 1) / kK;
   // row blocks: at most this many (every expert may end inside one)
-  const int64_t tiles = p.n_blk * (MODE == kWgrad ? E * p.m_blk : R / kM + (E < R ? E : R));
+  *tiles = p.n_blk * (MODE == kWgrad ? E * p.m_blk : R / kM + (E < R ? E : R));
   // boxes of the row operand: about an expert's rows, so that few rows cost
   // few bytes; 8 .. 128
   p.box_a = 8;
@@ -1026,50 +1101,89 @@ cudaError_t launch_product(const LinParams& base, const void* a, const void* b, 
   }
   p.stages = LinCfg<64, true>::kRing / (p.a_stage + LinCfg<64, true>::kBBytes);
   if (p.stages > LinCfg<64, true>::kStages) p.stages = LinCfg<64, true>::kStages;
-
-  CUtensorMap ta, tb;
-  cudaError_t err;
+  *out = p;
   if (MODE == kWgrad) {
-    err = encode_tmap_2d_bf16(&ta, a, p.n_w, R, 64, 64);
-    if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, b, p.n_in, R, 64, 64);
-  } else {
-    err = encode_tmap_2d_bf16(&ta, a, kc, R, 64, p.box_a);
-    if (err == cudaSuccess)
-      err = encode_tmap_3d_bf16(&tb, b, p.n_in, p.n_w, E, 64,
-                                MODE == kDgrad ? 64 : (glu ? bn / 2 : bn));
+    const cudaError_t err = encode_tmap_2d_bf16(ta, a, p.n_w, R, 64, 64);
+    return err != cudaSuccess ? err : encode_tmap_2d_bf16(tb, b, p.n_in, R, 64, 64);
   }
+  const cudaError_t err = encode_tmap_2d_bf16(ta, a, kc, R, 64, p.box_a);
+  return err != cudaSuccess ? err
+                            : encode_tmap_3d_bf16(tb, b, p.n_in, p.n_w, E, 64,
+                                                  MODE == kDgrad ? 64 : (glu ? bn / 2 : bn));
+}
+
+template <int MODE>
+cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
+  if (MODE == kFwd && few_rows(base)) return launch_few(base, a, b, st);
+  const Choice c = choose(MODE, base, MODE == kFwd && base.act == BEAM_MOE_ACT_SWIGLU);
+  if (c.bn == 0) {
+    if (base.clear_status) {  // the counter has to be zero before the first pair starts
+      const cudaError_t e = cudaMemsetAsync(base.status, 0, kStatusWords * 4, st);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_linear_pair(MODE, base, a, b, st);
+  }
+  LinParams p;
+  CUtensorMap ta, tb;
+  int64_t tiles;
+  const cudaError_t err = set_up<MODE>(base, c, a, b, &p, &ta, &tb, &tiles);
   if (err != cudaSuccess) return err;
-  if (bn == 256) return launch_tiles<MODE, 256, false>(ta, tb, p, tiles, 1, st);
-  if (bn == 128) return launch_tiles<MODE, 128, false>(ta, tb, p, tiles, 1, st);
-  return launch_tiles<MODE, 64, true>(ta, tb, p, tiles, parts, st);
+  if (c.bn == 256) return launch_tiles<MODE, 256, false>(ta, tb, p, tiles, 1, st);
+  if (c.bn == 128) return launch_tiles<MODE, 128, false>(ta, tb, p, tiles, 1, st);
+  return launch_tiles<MODE, 64, true>(ta, tb, p, tiles, c.parts, st);
 }
 
-// dZ and, if asked for, dbias. CTAs for about four per SM walk the row blocks.
-template <int BLOCK>
-cudaError_t launch_act_blocks(const LinParams& p, const ActParams& a, int64_t blocks, float* dbias,
-                              cudaStream_t st) {
-  const int64_t cols = (p.n_out + kActCols - 1) / kActCols;
-  int64_t gx = (2 * kActPerSm * (int64_t)device_sm_count() + cols - 1) / cols;
-  if (gx > blocks) gx = blocks;
-  const dim3 grid((unsigned)gx, (unsigned)cols);
-  if (p.act == BEAM_MOE_ACT_SWIGLU)
-    act_backward_kernel<BLOCK, true><<<grid, kActThreads, 0, st>>>(p, a);
-  else
-    act_backward_kernel<BLOCK, false><<<grid, kActThreads, 0, st>>>(p, a);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || !dbias) return err;
-  const int64_t jx = (p.n_w + 31) / 32;
-  int64_t jy = (8 * (int64_t)device_sm_count() + jx - 1) / jx;
-  if (jy > p.E) jy = p.E;
-  bias_join_kernel<BLOCK>
-      <<<dim3((unsigned)jx, (unsigned)jy), kActThreads, 0, st>>>(p, a.part, dbias);
-  return cudaGetLastError();
+// Whether a backward's products go out in one launch: both split tiles over
+// clusters, and dbias (if asked for) is summed over 32-row blocks.
+bool joint_backward(const LinParams& p, int block, Choice* dx, Choice* dw) {
+  *dx = choose(kDgrad, p, false);
+  *dw = choose(kWgrad, p, false);
+  return dx->bn == 64 && dw->bn == 64 && block == 32;
 }
 
-cudaError_t launch_act_backward(const LinParams& p, const ActParams& a, int block, int64_t blocks,
-                                float* dbias, cudaStream_t st) {
-  return block == 32 ? launch_act_blocks<32>(p, a, blocks, dbias, st)
-                     : launch_act_blocks<128>(p, a, blocks, dbias, st);
+cudaError_t launch_joint(const LinParams& base, const Choice& cx, const Choice& cw, const void* dz,
+                         const void* x, const void* w, void* dx, void* dw, const float* part,
+                         float* dbias, cudaStream_t st) {
+  Joint j;
+  CUtensorMap xa, xb, wa, wb;
+  int64_t tx = 0, tw = 0;
+  LinParams p = base;
+  p.out = dx;
+  cudaError_t err = set_up<kDgrad>(p, cx, dz, w, &j.dx, &xa, &xb, &tx);
+  if (err != cudaSuccess) return err;
+  p.out = dw;
+  err = set_up<kWgrad>(p, cw, dz, x, &j.dw, &wa, &wb, &tw);
+  if (err != cudaSuccess) return err;
+  const int64_t cluster = cx.parts > cw.parts ? cx.parts : cw.parts;
+  auto whole = [&](int64_t n) { return (n + cluster - 1) / cluster * cluster; };
+  j.dx_ctas = (int)whole(tx * cx.parts);
+  j.dw_ctas = (int)whole(tw * cw.parts);
+  j.dw.clear_status = 0;
+  j.part = part;
+  j.dbias = dbias;
+  j.join_x = j.join_y = 0;
+  if (dbias) join_grid(base, &j.join_x, &j.join_y);
+  using C = LinCfg<64, true>;
+  static PerDevice configured;
+  int unused = 0;
+  err = per_device(configured, &unused, [](int*) {
+    return cudaFuncSetAttribute(linear_joint_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kSmemBytes);
+  });
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(j.dx_ctas + j.dw_ctas + whole((int64_t)j.join_x * j.join_y)));
+  return cudaLaunchKernelEx(&cfg, linear_joint_kernel, xa, xb, wa, wb, j);
 }
 
 struct LinLayout {
@@ -1211,10 +1325,17 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
     a.z = acted ? static_cast<const uint16_t*>(z) : nullptr;
     a.dz = acted ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
     a.part = dbias ? reinterpret_cast<float*>(base + L.part) : nullptr;
-    LIN_CUDA(beam::launch_act_backward(p, a, L.block, L.blocks, dbias, st));
+    LIN_CUDA(beam::launch_act_backward(p, a, L.block, L.blocks, st));
     p.clear_status = 0;
   }
   p.cols = cfg->n_in;
+  const float* part = reinterpret_cast<const float*>(base + L.part);
+  beam::Choice cx, cw;
+  if (dx && dw && beam::joint_backward(p, L.block, &cx, &cw)) {
+    LIN_CUDA(beam::launch_joint(p, cx, cw, dz, x, w, dx, dw, part, dbias, st));
+    return BEAM_MOE_OK;
+  }
+  if (dbias) LIN_CUDA(beam::launch_bias_join(p, part, L.block, dbias, st));
   if (dx) {
     p.out = dx;
     LIN_CUDA(beam::launch_product<beam::kDgrad>(p, dz, w, st));

@@ -29,6 +29,7 @@ struct LinParams {
   int n_blk, m_blk;        // column tiles; row tiles of dW_e (WGRAD)
   int box_a;               // rows per box of the row operand (FWD, DGRAD)
   int a_stage, stages;     // split: bytes of the row operand per stage, stages
+  int parts;               // split: CTAs per tile
   int act, fp16, out32;
   const float* bias;       // [E][n_w] or NULL
   const void* residual;    // [rows][n_out] or NULL
@@ -192,7 +193,7 @@ __device__ __forceinline__ void activate(int act, float* z) {
   switch (act) {
     case BEAM_MOE_ACT_RELU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) z[j] = z[j] > 0.0f ? z[j] : 0.0f;
+      for (int j = 0; j < N; ++j) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // a NaN stays one
       break;
     case BEAM_MOE_ACT_GELU:
 #pragma unroll
