@@ -394,8 +394,9 @@ _raw_stream = None  # (device) -> its current stream
 def _bind_torch():
     global _types, _device, _raw_stream
     import torch
-    _types = ((torch.bfloat16, torch.int16, torch.uint16), (torch.float16,),
-              (torch.float32,), (torch.int32,))
+    _types = (frozenset((torch.bfloat16, torch.int16, torch.uint16)),
+              frozenset((torch.float16,)), frozenset((torch.float32,)),
+              frozenset((torch.int32,)))
     _device = torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda d: torch.cuda.current_stream(d).cuda_stream)
@@ -412,7 +413,7 @@ def _begin(name, t):
     return t.get_device()
 
 
-def _tensor(name, t, kind, dev, *shape):
+def _tensor(name, t, kind, dev, shape):
     """Address of a contiguous tensor of this kind and shape on device dev;
     None passes."""
     if t is None:
@@ -421,7 +422,8 @@ def _tensor(name, t, kind, dev, *shape):
             and t.is_contiguous()):
         return t.data_ptr()
     raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}; "
-                     f"expected a contiguous {_types[kind][0]} {shape} on cuda:{dev}")
+                     f"expected a contiguous tensor {shape} of a type among "
+                     f"{sorted(map(str, _types[kind]))} on cuda:{dev}")
 
 
 def _need(name, t):
@@ -460,11 +462,11 @@ def beam_moe_permute(cfg, x, topk_ids, xp, pos, offsets, ws, stream=None):
     dev = _begin("x", x)
     T, H, K, d = x.shape[0], cfg.width, cfg.top_k, cfg.dtype
     _check(lib().beam_moe_permute(
-        cfg, T, _tensor("x", x, d, dev, T, H),
-        _tensor("topk_ids", _need("topk_ids", topk_ids), _I32, dev, T, K),
-        _tensor("xp", _need("xp", xp), d, dev, T * K, H),
-        _tensor("pos", _need("pos", pos), _I32, dev, T, K),
-        _tensor("offsets", _need("offsets", offsets), _I32, dev, cfg.n_experts + 1),
+        cfg, T, _tensor("x", x, d, dev, (T, H)),
+        _tensor("topk_ids", _need("topk_ids", topk_ids), _I32, dev, (T, K)),
+        _tensor("xp", _need("xp", xp), d, dev, (T * K, H)),
+        _tensor("pos", _need("pos", pos), _I32, dev, (T, K)),
+        _tensor("offsets", _need("offsets", offsets), _I32, dev, (cfg.n_experts + 1,)),
         *_workspace(ws, dev), _on(dev, stream)), "beam_moe_permute")
 
 
@@ -473,14 +475,14 @@ def beam_moe_permute_backward(cfg, dxp, pos, dx, stream=None):
     dev = _begin("dx", dx)
     T, rows, H, d = dx.shape[0], _need("dxp", dxp).shape[0], cfg.width, cfg.dtype
     _check(lib().beam_moe_permute_backward(
-        cfg, T, rows, _tensor("dxp", dxp, d, dev, rows, H),
-        _tensor("pos", _need("pos", pos), _I32, dev, T, cfg.top_k),
-        _tensor("dx", dx, d, dev, T, H), _on(dev, stream)), "beam_moe_permute_backward")
+        cfg, T, rows, _tensor("dxp", dxp, d, dev, (rows, H)),
+        _tensor("pos", _need("pos", pos), _I32, dev, (T, cfg.top_k)),
+        _tensor("dx", dx, d, dev, (T, H)), _on(dev, stream)), "beam_moe_permute_backward")
 
 
 def _y_kind(cfg, y):
     """FP32 for fp32 rows, else the configuration's dtype."""
-    return FP32 if y.dtype is _types[FP32][0] else cfg.dtype
+    return FP32 if y.dtype in _types[FP32] else cfg.dtype
 
 
 def beam_moe_combine(cfg, y, pos, w, out, stream=None):
@@ -490,9 +492,9 @@ def beam_moe_combine(cfg, y, pos, w, out, stream=None):
     T, rows, H, K = out.shape[0], _need("y", y).shape[0], cfg.width, cfg.top_k
     kind = _y_kind(cfg, y)
     _check(lib().beam_moe_combine(
-        cfg, T, rows, _tensor("y", y, kind, dev, rows, H), kind,
-        _tensor("pos", _need("pos", pos), _I32, dev, T, K), _tensor("w", w, FP32, dev, T, K),
-        _tensor("out", out, cfg.dtype, dev, T, H), _on(dev, stream)), "beam_moe_combine")
+        cfg, T, rows, _tensor("y", y, kind, dev, (rows, H)), kind,
+        _tensor("pos", _need("pos", pos), _I32, dev, (T, K)), _tensor("w", w, FP32, dev, (T, K)),
+        _tensor("out", out, cfg.dtype, dev, (T, H)), _on(dev, stream)), "beam_moe_combine")
 
 
 def beam_moe_combine_backward(cfg, dout, y, pos, w, dy, dw, stream=None):
@@ -503,10 +505,10 @@ def beam_moe_combine_backward(cfg, dout, y, pos, w, dy, dw, stream=None):
     T, rows, H, K = dout.shape[0], like.shape[0], cfg.width, cfg.top_k
     kind = _y_kind(cfg, like)
     _check(lib().beam_moe_combine_backward(
-        cfg, T, rows, _tensor("dout", dout, cfg.dtype, dev, T, H),
-        _tensor("y", y, kind, dev, rows, H), kind,
-        _tensor("pos", _need("pos", pos), _I32, dev, T, K), _tensor("w", w, FP32, dev, T, K),
-        _tensor("dy", dy, kind, dev, rows, H), _tensor("dw", dw, FP32, dev, T, K),
+        cfg, T, rows, _tensor("dout", dout, cfg.dtype, dev, (T, H)),
+        _tensor("y", y, kind, dev, (rows, H)), kind,
+        _tensor("pos", _need("pos", pos), _I32, dev, (T, K)), _tensor("w", w, FP32, dev, (T, K)),
+        _tensor("dy", dy, kind, dev, (rows, H)), _tensor("dw", dw, FP32, dev, (T, K)),
         _on(dev, stream)), "beam_moe_combine_backward")
 
 
@@ -539,11 +541,11 @@ def beam_moe_linear(cfg, x, w, y, ws, bias=None, residual=None, offsets=None, z=
     rows, E, N, d = x.shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
     K, M, out = cfg.n_in, cfg.n_out, FP32 if cfg.out_fp32 else d
     _check(lib().beam_moe_linear(
-        cfg, rows, _tensor("x", x, d, dev, rows, K),
-        _tensor("w", _need("w", w), d, dev, E, N, K), _tensor("bias", bias, FP32, dev, E, N),
-        _tensor("residual", residual, out, dev, rows, M),
-        _tensor("offsets", offsets, _I32, dev, E + 1),
-        _tensor("y", _need("y", y), out, dev, rows, M), _tensor("z", z, d, dev, rows, N),
+        cfg, rows, _tensor("x", x, d, dev, (rows, K)),
+        _tensor("w", _need("w", w), d, dev, (E, N, K)), _tensor("bias", bias, FP32, dev, (E, N)),
+        _tensor("residual", residual, out, dev, (rows, M)),
+        _tensor("offsets", offsets, _I32, dev, (E + 1,)),
+        _tensor("y", _need("y", y), out, dev, (rows, M)), _tensor("z", z, d, dev, (rows, N)),
         *_workspace(ws, dev), _on(dev, stream)), "beam_moe_linear")
 
 
@@ -555,10 +557,10 @@ def beam_moe_linear_backward(cfg, dy, x, w, ws, dx=None, dw=None, dbias=None, z=
     rows, E, N, d = dy.shape[0], cfg.n_experts, _weight_rows(cfg), cfg.dtype
     K, M = cfg.n_in, cfg.n_out
     _check(lib().beam_moe_linear_backward(
-        cfg, rows, _tensor("dy", dy, d, dev, rows, M), _tensor("x", x, d, dev, rows, K),
-        _tensor("w", w, d, dev, E, N, K), _tensor("z", z, d, dev, rows, N),
-        _tensor("offsets", offsets, _I32, dev, E + 1), _tensor("dx", dx, d, dev, rows, K),
-        _tensor("dw", dw, d, dev, E, N, K), _tensor("dbias", dbias, FP32, dev, E, N),
+        cfg, rows, _tensor("dy", dy, d, dev, (rows, M)), _tensor("x", x, d, dev, (rows, K)),
+        _tensor("w", w, d, dev, (E, N, K)), _tensor("z", z, d, dev, (rows, N)),
+        _tensor("offsets", offsets, _I32, dev, (E + 1,)), _tensor("dx", dx, d, dev, (rows, K)),
+        _tensor("dw", dw, d, dev, (E, N, K)), _tensor("dbias", dbias, FP32, dev, (E, N)),
         *_workspace(ws, dev), _on(dev, stream)), "beam_moe_linear_backward")
 
 
