@@ -101,13 +101,14 @@ struct alignas(16) PairTile {
 };
 static_assert(sizeof(PairTile) == 32, "two 16-byte pieces");
 
-// FWD, DGRAD: the row blocks of all experts, in order, go in groups of 8;
-// inside a group weight tile by weight tile, row blocks fastest. The pairs at
-// work at one time then share row blocks and weight tiles through L2, and
-// experts with few rows (bound by their weights' bytes) run beside experts
-// with many (bound by the tensor cores). WGRAD: expert by expert, groups of 8
-// column tiles, row tile by row tile. (Groups of 8 / 16 / 32 / 64, 8192 rows
-// over 32 experts, swiglu: 411 / 440 / 460 / 497 us.)
+// FWD, DGRAD: expert by expert, its row blocks in groups of 8; inside a group
+// weight tile by weight tile, row blocks fastest. The pairs at work at one time
+// then share row blocks and weight tiles through L2, and the weights are read
+// from HBM once for up to 2048 rows. (Groups over the experts' row blocks
+// alike, to run experts bound by bytes beside experts bound by the tensor
+// cores, split experts between groups: 1.4 times the bytes, no faster in a
+// short run and slower in a long one, under the power limit.) WGRAD: groups of
+// 8 column tiles, row tile by row tile.
 template <int MODE>
 __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const Segments& s,
                                                 int m_step) {
@@ -120,8 +121,9 @@ __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const
     local = t - d.e * per;
     blks = p.n_blk;
   } else {
-    local = t;
-    blks = s.rb[p.E];
+    d.e = find_expert(s.rb, p.E, t / m_blk);
+    local = t - s.rb[d.e] * m_blk;
+    blks = s.rb[d.e + 1] - s.rb[d.e];
   }
   const int g = local / (kGroup * m_blk);
   const int in_g = min(kGroup, blks - g * kGroup);
@@ -136,15 +138,14 @@ __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const
     d.n0 = nb * kPair;
     d.once = 0;
   } else {
-    d.e = find_expert(s.rb, p.E, nb);
-    const int i0 = (nb - s.rb[d.e]) * kPair;
+    const int i0 = nb * kPair;
     int lo, cnt;
     segment(p, d.e, lo, cnt);
     d.row0 = lo + i0;
     d.rows = min(kPair, cnt - i0);
     d.nk = p.nk;
     d.n0 = 0;
-    d.once = s.rb[d.e + 1] - s.rb[d.e] == 1;
+    d.once = blks == 1;
   }
   return d;
 }
