@@ -614,14 +614,19 @@ __global__ void __launch_bounds__(kFewThreads)
   const int n = (GLU ? 1 : 2) * min(slot, slots - 1);
   const int row0 = RT == 1 ? blockIdx.y : 0;
   int e = 0;
-  if (p.offsets) {  // the first expert whose segment holds the row
-    e = -1;
-    for (int e0 = 0; e0 < p.E && e < 0; e0 += 32) {
-      int lo = 0, cnt = 0;
-      if (e0 + lane < p.E) segment(p, e0 + lane, lo, cnt);
-      const unsigned hit = __ballot_sync(0xffffffffu, row0 >= lo && row0 < lo + cnt);
-      if (hit) e = e0 + __ffs(hit) - 1;
-    }
+  if (p.offsets) {
+    // the expert whose segment holds the row: the last of 32 spread out that
+    // starts no later, then those from it on
+    const int spread = (p.E + 31) / 32;
+    int lo = 0, cnt = 0;
+    if (lane * spread < p.E) segment(p, lane * spread, lo, cnt);
+    const unsigned early =
+        __ballot_sync(0xffffffffu, lane * spread < p.E && lo <= row0);
+    const int e0 = (early ? 31 - __clz(early) : 0) * spread;
+    cnt = 0;
+    if (lane < spread && e0 + lane < p.E) segment(p, e0 + lane, lo, cnt);
+    const unsigned hit = __ballot_sync(0xffffffffu, row0 >= lo && row0 - lo < cnt);
+    e = hit ? e0 + __ffs(hit) - 1 : -1;
     if (e < 0) return;  // behind the last expert's rows
   }
   const bool fp16 = p.fp16;

@@ -93,6 +93,8 @@ CASES = [
     ([4], 0, 2056, 40, "swiglu", "bf16"),
     ([0, 1, 0, 2, 0], 1, 328, 72, "gelu", "bf16"),  # up to four rows in all: one row at a time
     ([0] * 40 + [1, 1], 2, 136, 200, "swiglu", "fp16"),
+    ([1] + [0] * 510 + [2], 0, 64, 72, "silu", "bf16"),
+    ([0] * 200 + [1] + [0] * 112, 1, 72, 64, "none", "fp16"),
     ([5], 0, 5120, 264, "swiglu", "bf16"),
     ([129], 0, 72, 136, "silu", "bf16"),
     ([300], 0, 520, 1320, "gelu_tanh", "fp16"),
