@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // A small backward's products and bias sums in one launch: they only wait for
 // dZ, and each alone leaves SMs idle (39 x 136 x 2872, gelu, dZ included: 14.4 us,
-// in launches of their own 23.4; 1000 x 520 x 1320: 37.0 and 39.8).
+// in launches of their own 23.4; 1000 x 520 x 1320: 27.9 and 39.8).
 struct Joint {
   LinParams dx, dw;
   int dx_ctas, dw_ctas;  // whole clusters each; the CTAs behind them join dbias
@@ -1118,9 +1118,8 @@ cudaError_t set_up(const LinParams& base, const Choice& c, const void* a, const 
 }
 
 template <int MODE>
-cudaError_t launch_product(const LinParams& base, const void* a, const void* b, cudaStream_t st) {
-  if (MODE == kFwd && few_rows(base)) return launch_few(base, a, b, st);
-  const Choice c = choose(MODE, base, MODE == kFwd && base.act == BEAM_MOE_ACT_SWIGLU);
+cudaError_t launch_product(const LinParams& base, const Choice& c, const void* a, const void* b,
+                           cudaStream_t st) {
   if (c.bn == 0) {
     if (base.clear_status) {  // the counter has to be zero before the first pair starts
       const cudaError_t e = cudaMemsetAsync(base.status, 0, kStatusWords * 4, st);
@@ -1138,12 +1137,32 @@ cudaError_t launch_product(const LinParams& base, const void* a, const void* b, 
   return launch_tiles<MODE, 64, true>(ta, tb, p, tiles, c.parts, st);
 }
 
-// Whether a backward's products go out in one launch: both split tiles over
-// clusters, and dbias (if asked for) is summed over 32-row blocks.
-bool joint_backward(const LinParams& p, int block, Choice* dx, Choice* dw) {
+int64_t split_ctas(int mode, const LinParams& p, const Choice& c) {
+  const int64_t n_blk = (p.cols + 63) / 64, R = p.rows, E = p.E;
+  const int64_t m = mode == kWgrad ? E * ((p.n_w + kM - 1) / kM) : R / kM + (E < R ? E : R);
+  return n_blk * m * c.parts;
+}
+
+// The forms of a backward's products, whichever of its results are asked for
+// (so that each comes out the same). True: they can go out in one launch, both
+// splitting tiles over clusters and dbias summed over 32-row blocks. Then the
+// splits are taken back, those with the fewest steps each first, until all
+// CTAs are resident at once (1000 x 520 x 1320, gelu: 36.7 us with 384 CTAs,
+// 27.9 with 285; 64 x 2000 x 1000: 21.9 and 17.1).
+bool choose_backward(const LinParams& p, int block, Choice* dx, Choice* dw) {
   *dx = choose(kDgrad, p, false);
   *dw = choose(kWgrad, p, false);
-  return dx->bn == 64 && dw->bn == 64 && block == 32;
+  if (dx->bn != 64 || dw->bn != 64 || block != 32) return false;
+  int jx, jy;
+  join_grid(p, &jx, &jy);
+  const int64_t sx = (p.n_w + kK - 1) / kK, sw = (p.rows / p.E + kK - 1) / kK;
+  while ((dx->parts > 1 || dw->parts > 1) &&
+         split_ctas(kDgrad, p, *dx) + split_ctas(kWgrad, p, *dw) + jx * jy >
+             2 * (int64_t)device_sm_count()) {
+    Choice* c = dw->parts == 1 || (dx->parts > 1 && sx / dx->parts < sw / dw->parts) ? dx : dw;
+    c->parts /= 2;
+  }
+  return true;
 }
 
 cudaError_t launch_joint(const LinParams& base, const Choice& cx, const Choice& cw, const void* dz,
@@ -1296,7 +1315,12 @@ beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int64_t rows, co
   p.z = z;
   p.out = y;
   p.clear_status = 1;
-  LIN_CUDA(beam::launch_product<beam::kFwd>(p, x, w, st));
+  if (beam::few_rows(p)) {
+    LIN_CUDA(beam::launch_few(p, x, w, st));
+    return BEAM_MOE_OK;
+  }
+  const beam::Choice c = beam::choose(beam::kFwd, p, cfg->act == BEAM_MOE_ACT_SWIGLU);
+  LIN_CUDA(beam::launch_product<beam::kFwd>(p, c, x, w, st));
   return BEAM_MOE_OK;
 }
 
@@ -1336,19 +1360,20 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
   p.cols = cfg->n_in;
   const float* part = reinterpret_cast<const float*>(base + L.part);
   beam::Choice cx, cw;
-  if (dx && dw && beam::joint_backward(p, L.block, &cx, &cw)) {
+  const bool joint = beam::choose_backward(p, L.block, &cx, &cw);
+  if (joint && dx && dw) {
     LIN_CUDA(beam::launch_joint(p, cx, cw, dz, x, w, dx, dw, part, dbias, st));
     return BEAM_MOE_OK;
   }
   if (dbias) LIN_CUDA(beam::launch_bias_join(p, part, L.block, dbias, st));
   if (dx) {
     p.out = dx;
-    LIN_CUDA(beam::launch_product<beam::kDgrad>(p, dz, w, st));
+    LIN_CUDA(beam::launch_product<beam::kDgrad>(p, cx, dz, w, st));
     p.clear_status = 0;
   }
   if (dw) {
     p.out = dw;
-    LIN_CUDA(beam::launch_product<beam::kWgrad>(p, dz, x, st));
+    LIN_CUDA(beam::launch_product<beam::kWgrad>(p, cw, dz, x, st));
   }
   return BEAM_MOE_OK;
 }
