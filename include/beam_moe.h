@@ -546,7 +546,7 @@ typedef enum beam_moe_act {
 } beam_moe_act;
 
 /* Supported: n_in and n_out multiples of 8 up to 65536, n_experts 1..512,
- * dtype bf16 or fp16, up to 2^26 rows. */
+ * dtype bf16 or fp16, up to 2^22 rows. */
 typedef struct beam_moe_linear_cfg {
   int32_t n_in;      /* width of X                                            */
   int32_t n_out;     /* width of Y                                            */
@@ -559,8 +559,9 @@ typedef struct beam_moe_linear_cfg {
 /*
  * Rows offsets[e] .. offsets[e+1]-1 through expert e:
  *   Z = X W_e^T + bias_e,  Y = act(Z) + residual.
- * Tensor-core products with FP32 accumulation; bias, activation and residual
- * are added in FP32 before the one rounding. N is n_out, 2 n_out for swiglu
+ * Tensor-core products with FP32 accumulation (whose error grows with the
+ * length of a sum, by up to 1.2e-9 of it per term: 3e-6 at n_in = 2560); bias,
+ * activation and residual are added in FP32 before the one rounding. N is n_out, 2 n_out for swiglu
  * (weight rows 0..n_out-1 gate, n_out..2 n_out-1 up, as W13 of the block).
  *   x        [rows][n_in], w [E][N][n_in], device
  *   bias     [E][N] fp32, residual [rows][n_out], or NULL
@@ -586,7 +587,9 @@ BEAM_MOE_API beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int
  * Gradients of beam_moe_linear (the residual's gradient is dY itself):
  *   dZ = dY act'(Z), dX = dZ W_e, dW_e = dZ^T X and dbias_e = sum dZ over the
  * rows of e (zero for an expert without rows). dZ is rounded to dtype once as
- * the products' operand; dbias sums it unrounded in FP32.
+ * the products' operand; dbias sums it unrounded in FP32. dW's sums over an
+ * expert's rows have the accumulators' error above: below fp16's half step up
+ * to 2^18 rows of one expert, below bf16's up to 2^20.
  *   dy       [rows][n_out] of dtype; x, w, offsets as above
  *   z        [rows][N] of dtype, beam_moe_linear's; NULL only with act none
  *   dx       [rows][n_in], dw [E][N][n_in] of dtype, dbias [E][N] fp32 (out);

@@ -90,7 +90,7 @@ def test_linear_calls_refuse_bad_arguments():
     st, need = lin_ws(c, 1000)
     stb, needb = lin_ws(c, 1000, 1)
     assert st == stb == OK and needb >= need + 1000 * 256 * 2
-    assert lin_ws(c, -1)[0] == INVALID and lin_ws(c, (1 << 26) + 1)[0] == UNSUPPORTED
+    assert lin_ws(c, -1)[0] == INVALID and lin_ws(c, (1 << 22) + 1)[0] == UNSUPPORTED
     assert lin_ws(c, 1000, 2)[0] == INVALID
     f, b = L.beam_moe_linear, L.beam_moe_linear_backward
     assert f(r, 0, None, None, None, None, None, None, None, None, 0, None) == OK
