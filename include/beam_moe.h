@@ -567,7 +567,10 @@ typedef struct beam_moe_linear_cfg {
  *   bias     [E][N] fp32, residual [rows][n_out], or NULL
  *   offsets  [E+1] int32, device, ascending (beam_moe_permute's); NULL with
  *            E = 1: all rows. Rows outside every expert's are left as they
- *            were. What points outside [0, rows] is cut off there.
+ *            were. Whatever offsets holds, no row has two experts and
+ *            nothing outside the buffers is touched: what points outside
+ *            [0, rows] is cut off there, and what lies before the end of an
+ *            earlier expert's rows is not counted again.
  *   y        [rows][n_out] (out); z [rows][N] of dtype (out), or NULL: Z for
  *            the backward call. y may be the residual's buffer.
  *   ws       beam_moe_linear_workspace_size(cfg, rows, 0) bytes; its status

@@ -100,7 +100,8 @@ __device__ __forceinline__ Tile decode(int t, const LinParams& p, const Segments
   d.n0 = nb * bn_out;
   d.once = m_blks == 1;
   if (MODE == kWgrad) {
-    segment(p, e, d.k0, d.kcnt);
+    d.k0 = s.lo[e];
+    d.kcnt = s.cnt[e];
     d.nk = (d.kcnt + kK - 1) / kK;
     d.row0 = mb * kM;
     d.rows = min(kM, p.n_w - d.row0);
@@ -284,14 +285,12 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
   }
-  if (MODE != kWgrad) {
-    if (p.offsets) {
-      build_segments<kThreads, kM>(p, seg, scratch);
-    } else if (threadIdx.x == 0) {
-      seg.lo[0] = seg.rb[0] = 0;
-      seg.cnt[0] = p.rows;
-      seg.rb[1] = (p.rows + kM - 1) / kM;
-    }
+  if (p.offsets) {
+    build_segments<kThreads, kM>(p, seg, scratch);
+  } else if (threadIdx.x == 0) {
+    seg.lo[0] = seg.rb[0] = 0;
+    seg.cnt[0] = p.rows;
+    seg.rb[1] = (p.rows + kM - 1) / kM;
   }
   if (p.clear_status && bid == 0) clear_status_area(p);
   tc_fence_before();
@@ -615,19 +614,29 @@ __global__ void __launch_bounds__(kFewThreads)
   const int row0 = RT == 1 ? blockIdx.y : 0;
   int e = 0;
   if (p.offsets) {
-    // the expert whose segment holds the row: the last of 32 spread out that
-    // starts no later, then those from it on
-    const int spread = (p.E + 31) / 32;
-    int lo = 0, cnt = 0;
-    if (lane * spread < p.E) segment(p, lane * spread, lo, cnt);
-    const unsigned early =
-        __ballot_sync(0xffffffffu, lane * spread < p.E && lo <= row0);
-    const int e0 = (early ? 31 - __clz(early) : 0) * spread;
-    cnt = 0;
-    if (lane < spread && e0 + lane < p.E) segment(p, e0 + lane, lo, cnt);
-    const unsigned hit = __ballot_sync(0xffffffffu, row0 >= lo && row0 - lo < cnt);
-    e = hit ? e0 + __ffs(hit) - 1 : -1;
-    if (e < 0) return;  // behind the last expert's rows
+    // the expert whose segment holds the row; each lane looks at every 32nd
+    int found = -1;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = lane; i < p.E; i += 32) {
+      int a, b;
+      cut_off(p, i, a, b);
+      bad |= b < a;
+      if (row0 >= a && row0 < b) found = i;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      found = -1;
+      int end = 0;
+#pragma unroll 1
+      for (int i = 0; i < p.E; ++i) {
+        int a, b, lo, cnt;
+        cut_off(p, i, a, b);
+        take_segment(a, b, end, lo, cnt);
+        if (row0 >= lo && row0 - lo < cnt) found = i;
+      }
+    }
+    e = __reduce_max_sync(0xffffffffu, found);
+    if (e < 0) return;  // no expert's row
   }
   const bool fp16 = p.fp16;
   const int nv = p.n_in / 8;  // 16-byte vectors of a row
@@ -773,7 +782,7 @@ __global__ void __launch_bounds__(kActThreads, kActPerSm)
   __shared__ int tab[kMaxE + 1 + 8];
   __shared__ float s_sum[8][GLU ? 2 : 1][kActCols + 8];
   const Segments seg = {nullptr, nullptr, tab};
-  build_segments<kActThreads, BLOCK>(p, seg, tab + kMaxE + 1);
+  const bool ordered = build_segments<kActThreads, BLOCK>(p, seg, tab + kMaxE + 1);
   if (p.clear_status && blockIdx.x == 0 && blockIdx.y == 0) clear_status_area(p);
   const bool fp16 = p.fp16;
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -782,7 +791,7 @@ __global__ void __launch_bounds__(kActThreads, kActPerSm)
   for (int q = blockIdx.x; q < total; q += gridDim.x) {
     const int e = find_expert(seg.rb, p.E, q);
     int lo, cnt;
-    segment(p, e, lo, cnt);
+    segment(p, e, ordered, lo, cnt);
     const int i0 = (q - seg.rb[e]) * BLOCK;
     const int64_t row0 = lo + i0;
     const int nrows = min(BLOCK, cnt - i0);

@@ -50,20 +50,57 @@ __device__ __forceinline__ void clear_status_area(const LinParams& p) {
 }
 
 // ------------------------------------------------------------- the segments
-// Segment of expert e, clamped into the rows there are whatever offsets holds.
-__device__ __forceinline__ void segment(const LinParams& p, int e, int& lo, int& cnt) {
-  if (!p.offsets) {
-    lo = 0;
-    cnt = p.rows;
-    return;
+// Whatever the offsets hold, no row has two experts and no row lies outside the
+// buffers: expert e's rows are those in [offsets[e], offsets[e + 1]), cut off at
+// the rows there are, that lie behind every expert's before it. Offsets that
+// ascend (`ordered`) need no look at the experts before; others are walked one
+// by one. Row blocks are then at most rows / BLOCK + min(E, rows), which is what
+// grids and the workspace are sized for.
+__device__ __forceinline__ void cut_off(const LinParams& p, int e, int& a, int& b) {
+  a = 0;
+  b = p.rows;
+  if (p.offsets) {
+    a = min(max(__ldg(p.offsets + e), 0), p.rows);
+    b = min(max(__ldg(p.offsets + e + 1), 0), p.rows);
   }
-  lo = min(max(__ldg(p.offsets + e), 0), p.rows);
-  cnt = min(max(__ldg(p.offsets + e + 1), lo), p.rows) - lo;
+}
+
+// The rows [lo, lo + cnt) that expert e gets of its [a, b), and where the rows
+// of the experts up to it end.
+__device__ __forceinline__ void take_segment(int a, int b, int& end, int& lo, int& cnt) {
+  lo = max(a, end);
+  cnt = max(b - lo, 0);
+  if (b > a) end = max(end, b);
+}
+
+__device__ __forceinline__ void segment(const LinParams& p, int e, bool ordered, int& lo,
+                                        int& cnt) {
+  int a, b, end = 0;
+  if (!ordered)
+#pragma unroll 1
+    for (int i = 0; i < e; ++i) {
+      cut_off(p, i, a, b);
+      take_segment(a, b, end, lo, cnt);
+    }
+  cut_off(p, e, a, b);
+  take_segment(a, b, end, lo, cnt);
+}
+
+// Whether the offsets ascend; all threads of the CTA call it (a barrier).
+__device__ __forceinline__ bool offsets_ordered(const LinParams& p) {
+  bool bad = false;
+  if (p.offsets)
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      int a, b;
+      cut_off(p, e, a, b);
+      bad |= b < a;
+    }
+  return !__syncthreads_or(bad);
 }
 
 // In shared memory: first row and row count of every expert (unless lo is
 // NULL), and the prefix of its BLOCK-row blocks (rb[E]: all of them). THREADS
-// threads call it.
+// threads call it; returns whether the offsets are ordered.
 struct Segments {
   int* lo;
   int* cnt;
@@ -71,22 +108,24 @@ struct Segments {
 };
 
 template <int THREADS, int BLOCK>
-__device__ __forceinline__ void build_segments(const LinParams& p, const Segments& s, int* scratch) {
+__device__ __forceinline__ bool build_segments(const LinParams& p, const Segments& s, int* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int PER = (kMaxE + THREADS - 1) / THREADS;
   int blocks[PER], sum = 0;
+  bool bad = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = tid * PER + i;
     blocks[i] = 0;
     if (e < p.E) {
-      int lo, cnt;
-      segment(p, e, lo, cnt);
+      int a, b;
+      cut_off(p, e, a, b);
+      bad |= b < a;
       if (s.lo) {
-        s.lo[e] = lo;
-        s.cnt[e] = cnt;
+        s.lo[e] = a;
+        s.cnt[e] = b - a;
       }
-      blocks[i] = (cnt + BLOCK - 1) / BLOCK;
+      blocks[i] = (b - a + BLOCK - 1) / BLOCK;
     }
     sum += blocks[i];
   }
@@ -97,7 +136,26 @@ __device__ __forceinline__ void build_segments(const LinParams& p, const Segment
     if (lane >= o) inc += n;
   }
   if (lane == 31) scratch[warp] = inc;
-  __syncthreads();
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      int end = 0, run = 0;
+#pragma unroll 1
+      for (int e = 0; e < p.E; ++e) {
+        int a, b, lo, cnt;
+        cut_off(p, e, a, b);
+        take_segment(a, b, end, lo, cnt);
+        if (s.lo) {
+          s.lo[e] = lo;
+          s.cnt[e] = cnt;
+        }
+        s.rb[e] = run;
+        run += (cnt + BLOCK - 1) / BLOCK;
+      }
+      s.rb[p.E] = run;
+    }
+    __syncthreads();
+    return false;
+  }
   int run = inc - sum;
   for (int w = 0; w < warp; ++w) run += scratch[w];
 #pragma unroll
@@ -110,6 +168,7 @@ __device__ __forceinline__ void build_segments(const LinParams& p, const Segment
     }
   }
   __syncthreads();
+  return true;
 }
 
 // The expert whose row blocks hold block q (rb[0] <= q < rb[E]).

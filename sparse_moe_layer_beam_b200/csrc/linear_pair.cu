@@ -117,7 +117,7 @@ static_assert(sizeof(PairTile) == 32, "two 16-byte pieces");
 // 8 column tiles, row tile by row tile.
 template <int MODE>
 __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const Segments& s,
-                                                int m_step) {
+                                                bool ordered, int m_step) {
   PairTile d;
   const int m_blk = p.m_blk;
   int blks, local;
@@ -139,14 +139,14 @@ __device__ __forceinline__ PairTile decode_pair(int t, const LinParams& p, const
   d.m0 = mb * m_step;
   d.unused = 0;
   if (MODE == kWgrad) {
-    segment(p, d.e, d.row0, d.rows);
+    segment(p, d.e, ordered, d.row0, d.rows);
     d.nk = (d.rows + kK - 1) / kK;
     d.n0 = nb * kPair;
     d.once = 0;
   } else {
     const int i0 = nb * kPair;
     int lo, cnt;
-    segment(p, d.e, lo, cnt);
+    segment(p, d.e, ordered, lo, cnt);
     d.row0 = lo + i0;
     d.rows = min(kPair, cnt - i0);
     d.nk = p.nk;
@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
   }
-  if (MODE != kWgrad) build_segments<kThreads, kPair>(p, seg, tab + kMaxE + 1);
+  const bool ordered = MODE == kWgrad ? offsets_ordered(p)
+                                      : build_segments<kThreads, kPair>(p, seg, tab + kMaxE + 1);
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
                                1000000000ull, true);
     PairTile t = {-1, 0, 0, 0, 0, 0, 0, 0};
     if (!__all_sync(0xffffffffu, got)) return t;
-    if (index < total) t = decode_pair<MODE>(index, p, seg, m_step);
+    if (index < total) t = decode_pair<MODE>(index, p, seg, ordered, m_step);
     if (lane == 0) {
       const int4 a = make_int4(t.e, t.m0, t.n0, t.row0), b = make_int4(t.rows, t.nk, t.once, 0);
       int4* slot = reinterpret_cast<int4*>(&ring[tslot]);

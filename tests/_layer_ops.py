@@ -21,6 +21,19 @@ def places(ids, E):
     return pos.reshape(np.asarray(ids).shape), np.array(offsets), np.array(src, np.int64)
 
 
+def segments(offsets, rows):
+    """[(lo, hi)] of every expert: its rows of [offsets[e], offsets[e + 1]), cut off at [0, rows],
+    that lie behind every expert's before it."""
+    o = [min(max(int(v), 0), rows) for v in offsets]
+    got, end = [], 0
+    for a, b in zip(o, o[1:]):
+        lo = max(a, end)
+        got.append((lo, max(b, lo)))
+        if b > a:
+            end = max(end, b)
+    return got
+
+
 def combine(y, pos, w):
     """(sum_k w y[pos], sum_k |w y[pos]|) in 64 bits."""
     T, K = pos.shape

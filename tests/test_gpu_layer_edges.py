@@ -1,0 +1,65 @@
+"""The row and linear operators on the GPU at the limits of what their documentation allows.
+
+Inputs are small whole numbers unless stated, so that every FP32 sum is exact whatever its order
+and results equal the 64-bit ones rounded once, bit for bit.
+"""
+import pytest
+import torch
+
+import sparse_moe_layer_beam_b200 as bm
+from tests import _layer_ops as ref
+from tests.test_layer_ops_limits import offset_vectors
+
+pytestmark = pytest.mark.gpu
+LEFT = 7.0
+BF = torch.bfloat16
+
+
+def whole(shape, seed, t=BF):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g).to(t)
+
+
+# rows, experts, n_in, n_out: the few-row form, split tiles, 128- and 256-column tiles, CTA pairs
+SHAPES = [(3, 40, 64, 72), (100, 512, 64, 64), (130, 4, 72, 136), (700, 60, 320, 328),
+          (1417, 10, 256, 2600), (3000, 3, 1032, 1288)]
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("R,E,n_in,n_out", SHAPES)
+def test_offsets_that_do_not_ascend(R, E, n_in, n_out, act):
+    """No row has two experts, and nothing is written outside the buffers: the workspace is the
+    front of a larger one with a pattern behind it."""
+    cfg = bm.linear_cfg(n_in, n_out, E, act)
+    x, w, dy = whole((R, n_in), 1), whole((E, n_out, n_in), 2), whole((R, n_out), 3)
+    z = whole((R, n_out), 4)
+    xd, wd, dyd, zd = x.cuda(), w.cuda(), dy.cuda(), z.cuda()
+    need = bm.beam_moe_linear_workspace_size(cfg, R, True)
+    big = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = big[:need]
+    for i, off in enumerate(offset_vectors(E, R, R)):
+        if 4 <= i < 38:  # eight of the 42
+            continue
+        offd = torch.tensor(off, dtype=torch.int32, device="cuda")
+        y = torch.full((R, n_out), LEFT, dtype=BF, device="cuda")
+        dx = torch.full((R, n_in), LEFT, dtype=BF, device="cuda")
+        dw = torch.full((E, n_out, n_in), LEFT, dtype=BF, device="cuda")
+        db = torch.full((E, n_out), LEFT, device="cuda")
+        bm.beam_moe_linear(cfg, xd, wd, y, ws, offsets=offd)
+        assert bm.beam_moe_check(ws) == 0
+        bm.beam_moe_linear_backward(cfg, dyd, xd, wd, ws, dx=dx, dw=dw, dbias=db, offsets=offd,
+                                    z=zd if act == "relu" else None)
+        assert bm.beam_moe_check(ws) == 0
+        assert bool((big[need:] == 0xA5).all())
+        wy, wdx = torch.full((R, n_out), LEFT, dtype=BF), torch.full((R, n_in), LEFT, dtype=BF)
+        wdw, wdb = torch.zeros((E, n_out, n_in)), torch.zeros((E, n_out))
+        dz = torch.where(z > 0, dy, 0.0) if act == "relu" else dy
+        for e, (a, b) in enumerate(ref.segments(off, R)):
+            if a == b:
+                continue
+            wy[a:b] = ref.act(x[a:b].float() @ w[e].float().T, act).to(BF)
+            wdx[a:b] = (dz[a:b].float() @ w[e].float()).to(BF)
+            wdw[e] = dz[a:b].float().T @ x[a:b].float()
+            wdb[e] = dz[a:b].float().sum(0)
+        assert torch.equal(y.cpu(), wy) and torch.equal(dx.cpu(), wdx)
+        assert torch.equal(dw.cpu(), wdw.to(BF)) and torch.equal(db.cpu(), wdb)

@@ -1,0 +1,36 @@
+"""The row and linear operators at the limits of what their documentation allows, on the host:
+offsets that do not ascend, sizes, first use by several threads (no GPU needed)."""
+import random
+
+import pytest
+
+import sparse_moe_layer_beam_b200 as bm
+from tests import _layer_ops as ref
+
+
+def offset_vectors(E, rows, seed):
+    """Offsets that break every promise: each second expert has all rows, descending ones, and
+    random ones that point outside [0, rows], too."""
+    rng = random.Random(seed)
+    yield [rows * (e % 2) for e in range(E + 1)]
+    yield [rows - e * rows // E for e in range(E + 1)]
+    for _ in range(20):
+        yield [rng.randint(-rows, 2 * rows) for _ in range(E + 1)]
+        yield [rng.choice((0, rows, 2 ** 31 - 1, -2 ** 31)) for _ in range(E + 1)]
+
+
+@pytest.mark.parametrize("E,rows,n_out", [(512, 100, 64), (4, 1000, 520), (32, 16384, 2560),
+                                          (3, 7, 8), (200, 40000, 1024)])
+def test_any_offsets_fit_the_workspace(E, rows, n_out):
+    """Segments lie one behind the other, so a backward's partial sums (a row of n_out floats per
+    block of 32 rows, or of 128 where there are enough of those) fit what it asks for."""
+    have = bm.beam_moe_linear_workspace_size(bm.linear_cfg(64, n_out, E), rows, True)
+    block = 32 if rows // 128 * -(-n_out // 256) < 512 else 128
+    for off in offset_vectors(E, rows, E + rows):
+        seg = ref.segments(off, rows)
+        assert all(0 <= a <= b <= rows for a, b in seg)
+        full = [s for s in seg if s[0] < s[1]]
+        assert all(p[1] <= q[0] for p, q in zip(full, full[1:]))
+        blocks = sum(-(-(b - a) // block) for a, b in seg)
+        assert blocks <= rows // block + min(E, rows)
+        assert 256 + blocks * n_out * 4 <= have
