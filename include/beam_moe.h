@@ -502,7 +502,9 @@ BEAM_MOE_API beam_moe_status beam_moe_permute(const beam_moe_rows_cfg* cfg, int6
 
 /* dx[t] = sum_k dxp[pos[t][k]] over the slots with a row, k ascending, summed
  * in FP32. dxp [rows][H], dx [T][H] (out), both of cfg->dtype; a pos outside
- * [0, rows) has no row. */
+ * [0, rows) has no row. In this call and the next two rows may be 0 (every
+ * assignment dropped): the row buffers may then be NULL, and dx, out and dw
+ * are zeros. */
 BEAM_MOE_API beam_moe_status beam_moe_permute_backward(const beam_moe_rows_cfg* cfg, int64_t T,
                                                        int64_t rows, const void* dxp,
                                                        const int32_t* pos, void* dx,
@@ -598,7 +600,7 @@ BEAM_MOE_API beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int
  *   dx       [rows][n_in], dw [E][N][n_in] of dtype, dbias [E][N] fp32 (out);
  *            any may be NULL, not all. x may be NULL without dw, w without dx.
  *   ws       beam_moe_linear_workspace_size(cfg, rows, 1) bytes
- * rows = 0 writes dw and dbias (zeros).
+ * rows = 0 writes dw and dbias (zeros); dx is empty then and may be NULL.
  */
 BEAM_MOE_API beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg,
                                                       int64_t rows, const void* dy,

@@ -1340,15 +1340,15 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
                                          const void* z, const int32_t* offsets, void* dx, void* dw,
                                          float* dbias, void* ws, size_t ws_bytes, void* stream) {
   LIN_TRY(beam::check_linear(cfg, rows));
-  if (!dx && !dw && !dbias) return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t n_w = (size_t)beam::weight_rows(*cfg), E = (size_t)cfg->n_experts;
-  if (rows == 0) {  // no rows: the sums over rows are zero
+  if (rows == 0) {  // no rows: the sums over rows are zero, dX is empty
     LIN_TRY(beam::check_ops_ptrs({}, {dw, dbias}));
     if (dw) LIN_CUDA(cudaMemsetAsync(dw, 0, E * n_w * cfg->n_in * 2, st));
     if (dbias) LIN_CUDA(cudaMemsetAsync(dbias, 0, E * n_w * 4, st));
     return BEAM_MOE_OK;
   }
+  if (!dx && !dw && !dbias) return BEAM_MOE_ERR_INVALID_ARG;
   if ((dw && !x) || (dx && !w)) return BEAM_MOE_ERR_INVALID_ARG;
   if (cfg->act != BEAM_MOE_ACT_NONE && !z) return BEAM_MOE_ERR_INVALID_ARG;
   LIN_TRY(beam::check_ops_ptrs({dy}, {x, w, z, offsets, dx, dw, dbias}));

@@ -645,7 +645,8 @@ beam_moe_status beam_moe_permute_backward(const beam_moe_rows_cfg* cfg, int64_t 
   if (s != BEAM_MOE_OK) return s;
   if (rows < 0) return BEAM_MOE_ERR_INVALID_ARG;
   if (T == 0) return BEAM_MOE_OK;
-  s = beam::check_ops_ptrs({dxp, pos, dx}, {});
+  // an empty buffer may have no address
+  s = rows == 0 ? beam::check_ops_ptrs({pos, dx}, {dxp}) : beam::check_ops_ptrs({dxp, pos, dx}, {});
   if (s != BEAM_MOE_OK) return s;
   return beam::cuda_status(beam::launch_combine_rows(*cfg, T, rows, dxp, cfg->dtype, pos, nullptr,
                                                      dx, reinterpret_cast<cudaStream_t>(stream)));
@@ -658,7 +659,7 @@ beam_moe_status beam_moe_combine(const beam_moe_rows_cfg* cfg, int64_t T, int64_
   if (s != BEAM_MOE_OK) return s;
   if (rows < 0 || !beam::y_type_ok(cfg, y_dtype)) return BEAM_MOE_ERR_INVALID_ARG;
   if (T == 0) return BEAM_MOE_OK;
-  s = beam::check_ops_ptrs({y, pos, out}, {w});
+  s = rows == 0 ? beam::check_ops_ptrs({pos, out}, {y, w}) : beam::check_ops_ptrs({y, pos, out}, {w});
   if (s != BEAM_MOE_OK) return s;
   return beam::cuda_status(beam::launch_combine_rows(*cfg, T, rows, y, y_dtype, pos, w, out,
                                                      reinterpret_cast<cudaStream_t>(stream)));
@@ -671,11 +672,12 @@ beam_moe_status beam_moe_combine_backward(const beam_moe_rows_cfg* cfg, int64_t 
   beam_moe_status s = beam::check_rows(cfg, T);
   if (s != BEAM_MOE_OK) return s;
   if (rows < 0 || !beam::y_type_ok(cfg, y_dtype)) return BEAM_MOE_ERR_INVALID_ARG;
-  if (!dy && !dw) return BEAM_MOE_ERR_INVALID_ARG;
-  if (dw && !y) return BEAM_MOE_ERR_INVALID_ARG;
   if (T == 0) return BEAM_MOE_OK;
+  // Without rows dy is empty, and y and dy may have no address.
+  if (rows != 0 && ((!dy && !dw) || (dw && !y))) return BEAM_MOE_ERR_INVALID_ARG;
   s = beam::check_ops_ptrs({dout, pos}, {y, w, dy, dw});
   if (s != BEAM_MOE_OK) return s;
+  if (rows == 0 && !dw) return BEAM_MOE_OK;
   return beam::cuda_status(beam::launch_combine_bwd(*cfg, T, rows, dout, y, y_dtype, pos, w, dy,
                                                     dw, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -63,3 +63,47 @@ def test_offsets_that_do_not_ascend(R, E, n_in, n_out, act):
             wdb[e] = dz[a:b].float().sum(0)
         assert torch.equal(y.cpu(), wy) and torch.equal(dx.cpu(), wdx)
         assert torch.equal(dw.cpu(), wdw.to(BF)) and torch.equal(db.cpu(), wdb)
+
+
+@pytest.mark.parametrize("H,dtype", [(5120, "bf16"), (33, "fp32"), (1002, "fp16")])
+def test_tokens_without_any_row(H, dtype):
+    """A rank that has none of the experts: rows = 0, every pos is -1 (or points at no row), and
+    an empty tensor has no address. The sums over no rows are zeros."""
+    t = {"bf16": BF, "fp16": torch.float16, "fp32": torch.float32}[dtype]
+    T, K = 37, 3
+    cfg = bm.rows_cfg(H, 16, K, dtype)
+    pos = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    pos[1, 2] = 0
+    none = torch.empty((0, H), dtype=t, device="cuda")
+    w = torch.full((T, K), float("nan"), device="cuda")
+    out = torch.full((T, H), LEFT, dtype=t, device="cuda")
+    bm.beam_moe_combine(cfg, none, pos, w, out)
+    assert not out.any()
+    out.fill_(LEFT)
+    bm.beam_moe_combine(cfg, torch.empty((0, H), device="cuda"), pos, None, out)
+    assert not out.any()
+    dx = torch.full((T, H), LEFT, dtype=t, device="cuda")
+    bm.beam_moe_permute_backward(cfg, none, pos, dx)
+    assert not dx.any()
+    dout = torch.full((T, H), float("nan"), dtype=t, device="cuda")
+    for y in (none, None):
+        dw = torch.full((T, K), LEFT, device="cuda")
+        bm.beam_moe_combine_backward(cfg, dout, y, pos, w, none, dw)
+        assert not dw.any()
+    bm.beam_moe_combine_backward(cfg, dout, none, pos, w, none, None)
+    e = torch.empty((0, K), dtype=torch.int32, device="cuda")
+    bm.beam_moe_combine_backward(cfg, none, none, e, None, none, None)
+
+
+@pytest.mark.parametrize("which", ["dx", "dw", "dbias"])
+def test_each_gradient_alone_without_rows(which):
+    cfg = bm.linear_cfg(64, 72, 2, "silu")
+    e = lambda n: torch.empty((0, n), dtype=BF, device="cuda")  # noqa: E731
+    out = {"dx": e(64), "dw": torch.ones((2, 72, 64), dtype=BF, device="cuda"),
+           "dbias": torch.ones((2, 72), device="cuda")}[which]
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, 0, True), dtype=torch.uint8,
+                     device="cuda")
+    w = torch.ones((2, 72, 64), dtype=BF, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    bm.beam_moe_linear_backward(cfg, e(72), e(64), w, ws, z=e(72), offsets=off, **{which: out})
+    assert not out.any()

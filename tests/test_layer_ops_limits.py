@@ -34,3 +34,14 @@ def test_any_offsets_fit_the_workspace(E, rows, n_out):
         blocks = sum(-(-(b - a) // block) for a, b in seg)
         assert blocks <= rows // block + min(E, rows)
         assert 256 + blocks * n_out * 4 <= have
+
+
+def test_nothing_to_do_is_no_error():
+    """Empty outputs may have no address: no tokens, or no rows with only their gradient asked."""
+    L, a = bm.lib(), 1 << 20
+    c = bm.rows_cfg(64, 8, 2)
+    assert L.beam_moe_combine_backward(c, 0, 0, None, None, 0, None, None, None, None, None) == 0
+    assert L.beam_moe_combine_backward(c, 5, 0, a, None, 0, a, a, None, None, None) == 0
+    lc = bm.linear_cfg(64, 128)
+    assert L.beam_moe_linear_backward(lc, 0, None, None, a, None, None, None, None, None, a, 256,
+                                      None) == 0
