@@ -599,7 +599,8 @@ BEAM_MOE_API beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int
  *   z        [rows][N] of dtype, beam_moe_linear's; NULL only with act none
  *   dx       [rows][n_in], dw [E][N][n_in] of dtype, dbias [E][N] fp32 (out);
  *            any may be NULL, not all. x may be NULL without dw, w without dx.
- *   ws       beam_moe_linear_workspace_size(cfg, rows, 1) bytes
+ *   ws       beam_moe_linear_workspace_size(cfg, rows, 1) bytes (which also
+ *            serve every smaller number of rows, and the forward call)
  * rows = 0 writes dw and dbias (zeros); dx is empty then and may be NULL.
  */
 BEAM_MOE_API beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg,

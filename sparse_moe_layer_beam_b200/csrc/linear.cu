@@ -1225,6 +1225,11 @@ struct LinLayout {
   int64_t blocks;  // row blocks at most
 };
 
+// Row blocks of E experts at most: every expert may end inside one.
+int64_t most_blocks(int64_t rows, int64_t E, int block) {
+  return rows / block + (E < rows ? E : rows);
+}
+
 int weight_rows(const beam_moe_linear_cfg& c) {
   return c.act == BEAM_MOE_ACT_SWIGLU ? 2 * c.n_out : c.n_out;
 }
@@ -1234,14 +1239,21 @@ LinLayout lin_layout(const beam_moe_linear_cfg& c, int64_t rows, bool backward) 
   const int64_t E = c.n_experts;
   // 32-row blocks while 128-row blocks would leave SMs without work (1000 x
   // 1320, gelu: 34 us with 128 rows)
-  L.block = rows / 128 * ((c.n_out + kActCols - 1) / kActCols) < 512 ? 32 : 128;
-  L.blocks = rows / L.block + (E < rows ? E : rows);
+  const int64_t cols = (c.n_out + kActCols - 1) / kActCols;
+  const int64_t wide_from = (512 + cols - 1) / cols * 128;  // rows from which blocks hold 128
+  L.block = rows < wide_from ? 32 : 128;
+  L.blocks = most_blocks(rows, E, L.block);
+  // A workspace serves every smaller number of rows too: the partial sums have
+  // room for the most blocks that any of them has.
+  int64_t room = L.blocks;
+  if (L.block == 128 && most_blocks(wide_from - 1, E, 32) > room)
+    room = most_blocks(wide_from - 1, E, 32);
   L.part = 256;
   L.dz = L.part;
   L.total = 256;
   if (backward) {
     const size_t n_w = (size_t)weight_rows(c);
-    L.dz = (L.part + (size_t)L.blocks * n_w * 4 + 1023) / 1024 * 1024;
+    L.dz = (L.part + (size_t)room * n_w * 4 + 1023) / 1024 * 1024;
     L.total = L.dz + (c.act == BEAM_MOE_ACT_NONE ? 0 : ((size_t)rows * n_w * 2 + 255) / 256 * 256);
   }
   return L;

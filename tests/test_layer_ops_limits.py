@@ -45,3 +45,21 @@ def test_nothing_to_do_is_no_error():
     lc = bm.linear_cfg(64, 128)
     assert L.beam_moe_linear_backward(lc, 0, None, None, a, None, None, None, None, None, a, 256,
                                       None) == 0
+
+
+@pytest.mark.parametrize("E,n_out,act", [(1, 5120, "none"), (32, 2560, "swiglu"), (512, 64, "gelu"),
+                                         (3, 8, "relu"), (256, 65536, "none"), (7, 520, "silu")])
+def test_a_workspace_serves_fewer_rows(E, n_out, act):
+    """A program keeps one workspace, sized for its largest batch: no smaller one asks for more.
+    (Row blocks of the backward change from 32 to 128 rows where rows // 128 * ceil(n_out / 256)
+    reaches 512.)"""
+    c = bm.linear_cfg(64, n_out, E, act)
+    switch = -(-512 // -(-n_out // 256)) * 128
+    rows = sorted({r for s in (1, switch, 4 * switch) for r in range(max(0, s - 300), s + 300)}
+                  | {2 ** i + d for i in range(22) for d in (-1, 0, 1)})
+    sizes = [bm.beam_moe_linear_workspace_size(c, r, True) for r in rows]
+    assert sizes == sorted(sizes)
+    assert all(bm.beam_moe_linear_workspace_size(c, r) <= s for r, s in zip(rows, sizes))
+    r = bm.rows_cfg(64, 512, 8)
+    sizes = [bm.beam_moe_permute_workspace_size(r, t) for t in range(900, 1200)]
+    assert sizes == sorted(sizes)
