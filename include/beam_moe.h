@@ -577,7 +577,7 @@ typedef struct beam_moe_linear_cfg {
  *            the backward call. y may be the residual's buffer.
  *   ws       beam_moe_linear_workspace_size(cfg, rows, 0) bytes; its status
  *            word reports through beam_moe_check
- * rows = 0 is a no-op.
+ * rows = 0 writes nothing but the status word (if ws is given).
  */
 BEAM_MOE_API beam_moe_status beam_moe_linear_workspace_size(const beam_moe_linear_cfg* cfg,
                                                             int64_t rows, int32_t backward,

@@ -1282,6 +1282,13 @@ beam_moe_status check_linear_ws(const beam_moe_linear_cfg* c, int64_t rows, bool
   return BEAM_MOE_OK;
 }
 
+// A call without rows launches no kernel that clears the status area; the
+// status word of a workspace that was given says so all the same.
+cudaError_t clear_status(void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!ws || ws_bytes < kStatusWords * 4) return cudaSuccess;
+  return cudaMemsetAsync(ws, 0, kStatusWords * 4, st);
+}
+
 LinParams lin_params(const beam_moe_linear_cfg& c, int64_t rows, const int32_t* offsets, void* ws) {
   LinParams p;
   memset(&p, 0, sizeof(p));
@@ -1327,10 +1334,10 @@ beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int64_t rows, co
                                 const int32_t* offsets, void* y, void* z, void* ws,
                                 size_t ws_bytes, void* stream) {
   LIN_TRY(beam::check_linear(cfg, rows));
-  if (rows == 0) return BEAM_MOE_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (rows == 0) return beam::cuda_status(beam::clear_status(ws, ws_bytes, st));
   LIN_TRY(beam::check_ops_ptrs({x, w, y}, {bias, residual, offsets, z}));
   LIN_TRY(beam::check_linear_ws(cfg, rows, false, offsets, ws, ws_bytes));
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   beam::LinParams p = beam::lin_params(*cfg, rows, offsets, ws);
   p.cols = cfg->n_out;
   p.bias = bias;
@@ -1356,6 +1363,7 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
   const size_t n_w = (size_t)beam::weight_rows(*cfg), E = (size_t)cfg->n_experts;
   if (rows == 0) {  // no rows: the sums over rows are zero, dX is empty
     LIN_TRY(beam::check_ops_ptrs({}, {dw, dbias}));
+    LIN_CUDA(beam::clear_status(ws, ws_bytes, st));
     if (dw) LIN_CUDA(cudaMemsetAsync(dw, 0, E * n_w * cfg->n_in * 2, st));
     if (dbias) LIN_CUDA(cudaMemsetAsync(dbias, 0, E * n_w * 4, st));
     return BEAM_MOE_OK;

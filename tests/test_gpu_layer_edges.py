@@ -107,3 +107,18 @@ def test_each_gradient_alone_without_rows(which):
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     bm.beam_moe_linear_backward(cfg, e(72), e(64), w, ws, z=e(72), offsets=off, **{which: out})
     assert not out.any()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_status_of_a_call_without_rows(backward):
+    """The status word of a workspace that held anything reports the call, not what was there."""
+    cfg = bm.linear_cfg(64, 72)
+    e = lambda n: torch.empty((0, n), dtype=BF, device="cuda")  # noqa: E731
+    w = torch.ones((1, 72, 64), dtype=BF, device="cuda")
+    ws = torch.full((bm.beam_moe_linear_workspace_size(cfg, 0, True),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    if backward:
+        bm.beam_moe_linear_backward(cfg, e(72), e(64), w, ws, dw=torch.empty_like(w))
+    else:
+        bm.beam_moe_linear(cfg, e(64), w, e(72), ws)
+    assert bm.beam_moe_check(ws) == 0

@@ -43,8 +43,8 @@ def test_nothing_to_do_is_no_error():
     assert L.beam_moe_combine_backward(c, 0, 0, None, None, 0, None, None, None, None, None) == 0
     assert L.beam_moe_combine_backward(c, 5, 0, a, None, 0, a, a, None, None, None) == 0
     lc = bm.linear_cfg(64, 128)
-    assert L.beam_moe_linear_backward(lc, 0, None, None, a, None, None, None, None, None, a, 256,
-                                      None) == 0
+    assert L.beam_moe_linear_backward(lc, 0, None, None, a, None, None, None, None, None, None,
+                                      0, None) == 0
 
 
 @pytest.mark.parametrize("E,n_out,act", [(1, 5120, "none"), (32, 2560, "swiglu"), (512, 64, "gelu"),
