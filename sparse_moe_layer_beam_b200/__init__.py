@@ -386,7 +386,7 @@ class Trace:
 
 _NAMES = {"bf16": BF16, "fp16": FP16, "fp32": FP32}
 _I32 = 3
-_types = None    # tensor types of each kind (bf16 also as its 16-bit pattern)
+_types = None    # tensor types of each kind (bf16 also as its 16-bit pattern); set last
 _device = None   # () -> current CUDA device
 _raw_stream = None  # (device) -> its current stream
 
@@ -394,12 +394,13 @@ _raw_stream = None  # (device) -> its current stream
 def _bind_torch():
     global _types, _device, _raw_stream
     import torch
-    _types = (frozenset((torch.bfloat16, torch.int16, torch.uint16)),
-              frozenset((torch.float16,)), frozenset((torch.float32,)),
-              frozenset((torch.int32,)))
     _device = torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda d: torch.cuda.current_stream(d).cuda_stream)
+    # last: another thread that finds the types finds the rest as well
+    _types = (frozenset((torch.bfloat16, torch.int16, torch.uint16)),
+              frozenset((torch.float16,)), frozenset((torch.float32,)),
+              frozenset((torch.int32,)))
 
 
 def _begin(name, t):

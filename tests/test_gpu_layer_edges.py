@@ -122,3 +122,38 @@ def test_status_of_a_call_without_rows(backward):
     else:
         bm.beam_moe_linear(cfg, e(64), w, e(72), ws)
     assert bm.beam_moe_check(ws) == 0
+
+
+def test_threads_at_once():
+    """Four threads, each on a stream, with tensors and a workspace of its own."""
+    import threading
+    R, n_in, n_out = (5, 90, 700, 1500), 1032, 1288
+    w = whole((1, n_out, n_in), 5)
+    wd, wrong, start = w.cuda(), [], threading.Barrier(len(R))
+    torch.cuda.synchronize()
+
+    def work(i):
+        x, dy = whole((R[i], n_in), 10 + i), whole((R[i], n_out), 20 + i)
+        cfg = bm.linear_cfg(n_in, n_out)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            xd, dyd = x.cuda(), dy.cuda()
+            ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R[i], True),
+                             dtype=torch.uint8, device="cuda")
+            start.wait(60)
+            for _ in range(20):
+                y, dx, dw = torch.empty_like(dyd), torch.empty_like(xd), torch.empty_like(wd)
+                bm.beam_moe_linear(cfg, xd, wd, y, ws)
+                bm.beam_moe_linear_backward(cfg, dyd, xd, wd, ws, dx=dx, dw=dw)
+            status = bm.beam_moe_check(ws)
+            same = (torch.equal(y.cpu(), (x.float() @ w[0].float().T).to(BF))
+                    and torch.equal(dx.cpu(), (dy.float() @ w[0].float()).to(BF))
+                    and torch.equal(dw.cpu()[0], (dy.float().T @ x.float()).to(BF)))
+        if status or not same:
+            wrong.append((i, status, same))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(R))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

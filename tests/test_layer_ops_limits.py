@@ -1,6 +1,7 @@
 """The row and linear operators at the limits of what their documentation allows, on the host:
 offsets that do not ascend, sizes, first use by several threads (no GPU needed)."""
 import random
+import sys
 
 import pytest
 
@@ -63,3 +64,26 @@ def test_a_workspace_serves_fewer_rows(E, n_out, act):
     r = bm.rows_cfg(64, 512, 8)
     sizes = [bm.beam_moe_permute_workspace_size(r, t) for t in range(900, 1200)]
     assert sizes == sorted(sizes)
+
+
+def test_first_use_by_several_threads(monkeypatch):
+    """A call takes the binding as ready once _types is there: at no line of its set-up may
+    another thread find that and not the rest."""
+    for name in ("_types", "_device", "_raw_stream"):
+        monkeypatch.setattr(bm, name, None)
+    half_ready = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is not bm._bind_torch.__code__:
+            return None
+        if bm._types is not None and (bm._device is None or bm._raw_stream is None):
+            half_ready.append(frame.f_lineno)
+        return trace
+
+    old = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        bm._bind_torch()
+    finally:
+        sys.settrace(old)
+    assert bm._types and bm._device and bm._raw_stream and not half_ready
