@@ -592,7 +592,7 @@ beam_moe_status check_rows(const beam_moe_rows_cfg* c, int64_t T) {
   if (c->dtype < BEAM_MOE_BF16 || c->dtype > BEAM_MOE_FP32) return BEAM_MOE_ERR_INVALID_ARG;
   if (c->width > 65536 || c->n_experts > kMaxE || c->top_k > kMaxK)
     return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
-  if (T * (int64_t)c->top_k > (int64_t)1 << 30) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T > ((int64_t)1 << 30) / c->top_k) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
   return BEAM_MOE_OK;
 }
 

@@ -87,3 +87,23 @@ def test_first_use_by_several_threads(monkeypatch):
     finally:
         sys.settrace(old)
     assert bm._types and bm._device and bm._raw_stream and not half_ready
+
+
+@pytest.mark.parametrize("T", [(1 << 28) + 1, 1 << 58, 1 << 60, (1 << 60) + 1, 1 << 62,
+                               (1 << 63) - 1])
+def test_more_tokens_than_are_supported(T):
+    """T * top_k beyond 2^30, where the product leaves 64 bits too."""
+    a, L = 1 << 20, bm.lib()
+    for K in (4, 16, 32):
+        c = bm.rows_cfg(64, 40, K)
+        with pytest.raises(bm.BeamMoeError) as e:
+            bm.beam_moe_permute_workspace_size(c, T)
+        assert e.value.status == 2
+        assert L.beam_moe_permute(c, T, a, a, a, a, a, a, 1 << 62, None) == 2
+        assert L.beam_moe_combine(c, T, 9, a, 0, a, a, a, None) == 2
+        assert L.beam_moe_combine_backward(c, T, 9, a, a, 0, a, a, a, a, None) == 2
+    assert bm.beam_moe_permute_workspace_size(bm.rows_cfg(64, 40, 4), 1 << 28) > 1 << 31
+    lc = bm.linear_cfg(64, 64)
+    with pytest.raises(bm.BeamMoeError) as e:
+        bm.beam_moe_linear_workspace_size(lc, T)
+    assert e.value.status == 2
