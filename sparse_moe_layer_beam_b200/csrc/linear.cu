@@ -751,9 +751,11 @@ __device__ __forceinline__ void act_grad8(int act, float* g, const float* z) {
     case BEAM_MOE_ACT_GELU_TANH:
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float s = tanh_gate(z[j]);  // its slope is s (1 - s) 2 da/dz
+        // its slope is s (1 - s) 2 da/dz; from |z| = 100 on s (1 - s) is zero, and the
+        // square must not become infinite beside it
+        const float s = tanh_gate(z[j]), zz = fminf(z[j] * z[j], 1e4f);
         g[j] *= fmaf(z[j] * s * (1.0f - s),
-                     1.59576912160573071f * fmaf(3.0f * 0.044715f, z[j] * z[j], 1.0f), s);
+                     1.59576912160573071f * fmaf(3.0f * 0.044715f, zz, 1.0f), s);
       }
       break;
     case BEAM_MOE_ACT_SILU:
@@ -828,8 +830,9 @@ __global__ void __launch_bounds__(kActThreads, kActPerSm)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float s = sigmoid_f(z[j]), d = g[j];
-              g[j] = d * u[j] * s * fmaf(z[j], 1.0f - s, 1.0f);
-              u[j] = d * z[j] * s;
+              // the slopes first: dY times a half may overflow where dZ does not
+              g[j] = d * (u[j] * (s * fmaf(z[j], 1.0f - s, 1.0f)));
+              u[j] = d * (z[j] * s);
               sumu[j] += u[j];
             }
           } else {

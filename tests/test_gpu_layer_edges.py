@@ -157,3 +157,37 @@ def test_threads_at_once():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_gradients_far_out(act):
+    """dZ where squares and cubes of Z, or products of dY and Z, leave FP32: finite, and the
+    formula's. One row, so that the bias's gradient is dZ in FP32; within 2^-18 of the terms that
+    dZ adds up. Where a sigmoid or a cdf lies below FP32's normal numbers, 2^-126, it may be zero:
+    a slope is at most |z| 2a'(z) times that there, 90 for silu (z < -87), 227 for gelu_tanh
+    (z < -9.9) and 15 for gelu, and |z| e^z only falls behind; so dZ is off by 256 2^-126 |dy up|
+    at most."""
+    z = torch.tensor([s * v for v in (1e2, 1e4, 1e10, 2e18, 2e19, 1e30, 3e38, 0.5)
+                      for s in (1, -1)])
+    dy = torch.full((z.numel(),), 4.0)
+    if act == "swiglu":
+        up = torch.tensor([1e-30, 3e38])
+        z = torch.cat((z.repeat(2), up.repeat_interleave(z.numel())))
+        dy = torch.cat((dy, torch.full_like(dy, 2.0 ** -10)))
+    z, dy = z[None].to(BF), dy[None].to(BF)
+    N, n_out = z.shape[1], dy.shape[1]
+    cfg = bm.linear_cfg(8, n_out, 1, act)
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, 1, True), dtype=torch.uint8,
+                     device="cuda")
+    db = torch.full((1, N), LEFT, device="cuda")
+    bm.beam_moe_linear_backward(cfg, dy.cuda(), None, None, ws, dbias=db, z=z.cuda())
+    want = ref.act_grad(dy.double(), z.double(), act)
+    terms = ref.act_grad_terms(dy.double(), z.double(), act)
+    # a result beyond FP32 is infinite
+    want = torch.where(want.abs() > torch.finfo(torch.float32).max, want.sign() * torch.inf, want)
+    got = db.cpu().double()
+    scale = dy.double().abs()
+    if act == "swiglu":
+        scale = (scale * z.double().chunk(2, -1)[1].abs().clamp(min=1)).repeat(1, 2)
+    fine = (got == want) | ((got - want).abs() <= 2.0 ** -18 * terms + 2.0 ** -118 * scale)
+    assert bool(fine.all()), list(zip(z[0].tolist(), got[0].tolist(), want[0].tolist()))
