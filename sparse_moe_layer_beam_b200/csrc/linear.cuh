@@ -229,7 +229,30 @@ __device__ __forceinline__ uint32_t idesc_of(bool fp16, bool a_mn, bool b_mn, ui
 }
 
 // ----------------------------------------------------------------- epilogue
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// e^-z. __expf rounds z log2(e) before it raises 2 to it, so its error grows with
+// |z|: 25 steps at z = -20. That is far below a half step of a 16-bit result,
+// where it is used (FULL false). FULL, for FP32 results and where a row or two
+// cost nothing, puts the rounding back (Cody
+// and Waite's two-part ln 2): with t = fl(-z log2 e), e^-z = 2^t e^(-z - t ln 2), and the second factor is
+// 1 + r to first order (r < 1e-5). Used for all results it cost 5 % where a
+// short contraction leaves the epilogue as the bound (16384 x 512 x 5120, swiglu:
+// 243 and 256 us); expf and a full division there 449 us. z is held to +-88,
+// beyond which the quotients below are 0 and 1 either way.
+template <bool FULL>
+__device__ __forceinline__ float exp_neg(float z) {
+  if (!FULL) return __expf(-z);
+  z = fminf(fmaxf(z, -88.0f), 88.0f);
+  const float t = z * -1.44269504088896341f;
+  const float r = fmaf(t, 1.90465429995776787e-9f, fmaf(t, -0.693147182464599609f, -z));
+  float p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+  return fmaf(p, r, p);
+}
+
+template <bool FULL = false>
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return __fdividef(1.0f, 1.0f + exp_neg<FULL>(z));
+}
 
 // 1/2 (1 + erf(z / sqrt 2)) as a complement: relative accuracy down the tail.
 __device__ __forceinline__ float normal_cdf(float z) {
@@ -237,17 +260,21 @@ __device__ __forceinline__ float normal_cdf(float z) {
 }
 
 // 1/2 (1 + tanh(a)) = sigmoid(2 a) for a = sqrt(2/pi) (z + 0.044715 z^3).
+template <bool FULL = false>
 __device__ __forceinline__ float tanh_gate(float z) {
-  return sigmoid_f(1.59576912160573071f * fmaf(0.044715f * z * z, z, z));
+  return sigmoid_f<FULL>(1.59576912160573071f * fmaf(0.044715f * z * z, z, z));
 }
 
-__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+template <bool FULL>
+__device__ __forceinline__ float silu_f(float z) {
+  return __fdividef(z, 1.0f + exp_neg<FULL>(z));
+}
 
 // act over N values. The choice is made once for all of them and the longer
 // formulas stay rolled: unrolled inside a switch per value they filled the
 // instruction cache and bounded the kernel (16384 x 5120 x 5120, act none:
 // 885 us against 590).
-template <int N>
+template <int N, bool FULL>
 __device__ __forceinline__ void activate(int act, float* z) {
   switch (act) {
     case BEAM_MOE_ACT_RELU:
@@ -260,13 +287,20 @@ __device__ __forceinline__ void activate(int act, float* z) {
       break;
     case BEAM_MOE_ACT_GELU_TANH:
 #pragma unroll
-      for (int j = 0; j < N; ++j) z[j] *= tanh_gate(z[j]);
+      for (int j = 0; j < N; ++j) z[j] *= tanh_gate<FULL>(z[j]);
       break;
     case BEAM_MOE_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) z[j] = silu_f(z[j]);
+      for (int j = 0; j < N; ++j) z[j] = silu_f<FULL>(z[j]);
       break;
   }
+}
+
+// z = silu(z) u over N values.
+template <int N, bool FULL>
+__device__ __forceinline__ void swiglu(float* z, const float* u) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) z[j] = silu_f<FULL>(z[j]) * u[j];
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool fp16) {

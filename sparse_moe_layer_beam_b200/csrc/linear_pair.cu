@@ -191,8 +191,9 @@ __device__ __forceinline__ void store_rows(void* p, int64_t at, int64_t ld, int 
   else store_rows<N, __nv_bfloat16>(p, at, ld, n, v);
 }
 
-// N rows (from row r0 of the tile) of one column of Y; v: act(Z).
-template <int N>
+// N rows (from row r0 of the tile) of one column of Y; v: act(Z). F32: the type
+// of Y and the residual.
+template <int N, bool F32>
 __device__ __forceinline__ void finish_rows(const LinParams& p, const PairTile& t, int col, int r0,
                                             float* v) {
   const int n = min(N, t.rows - r0);
@@ -200,12 +201,12 @@ __device__ __forceinline__ void finish_rows(const LinParams& p, const PairTile& 
   if (p.residual) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (j < n) v[j] += load1(p.residual, at + (int64_t)j * p.n_out, p.out32, p.fp16);
+      if (j < n) v[j] += load1(p.residual, at + (int64_t)j * p.n_out, F32, p.fp16);
   }
-  store_rows<N>(p.out, at, p.n_out, n, v, p.out32, p.fp16);
+  store_rows<N>(p.out, at, p.n_out, n, v, F32, p.fp16);
 }
 
-template <int MODE, bool GLU>
+template <int MODE, bool GLU, bool F32>
 __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b,
@@ -590,9 +591,8 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
             g[j] = lane < 16 ? f[j] : other;
             u[j] = lane < 16 ? other : f[8 + j];
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = silu_f(g[j]) * u[j];
-          if (live) finish_rows<8>(p, t, col, c0 + (lane >> 4) * 8, g);
+          swiglu<8, F32>(g, u);
+          if (live) finish_rows<8, F32>(p, t, col, c0 + (lane >> 4) * 8, g);
         }
       } else {
         const int col = t.m0 + (int)rank * 128 + q * 32 + lane;
@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
             if (p.z)
               store_rows<16>(p.z, (int64_t)(t.row0 + c0) * p.n_w + col, p.n_w, t.rows - c0, f,
                              false, p.fp16);
-            activate<16>(p.act, f);
-            finish_rows<16>(p, t, col, c0, f);
+            activate<16, F32>(p.act, f);
+            finish_rows<16, F32>(p, t, col, c0, f);
           }
         }
       }
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
   }
 }
 
-template <int MODE, bool GLU>
+template <int MODE, bool GLU, bool F32>
 cudaError_t run_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                       const LinParams& p, cudaStream_t st) {
   // Per device: the shared-memory attribute and the number of CTA pairs that
@@ -659,13 +659,13 @@ cudaError_t run_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
   int resident = 0;
   cudaError_t err = per_device(pairs, &resident, [&cfg](int* v) {
     cudaError_t e =
-        cudaFuncSetAttribute(linear_pair_kernel<MODE, GLU>,
+        cudaFuncSetAttribute(linear_pair_kernel<MODE, GLU, F32>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, PairMem<MODE>::kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t probe = cfg;
     probe.gridDim = dim3((unsigned)(device_sm_count() & ~1));
     int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, linear_pair_kernel<MODE, GLU>, &probe);
+    e = cudaOccupancyMaxActiveClusters(&clusters, linear_pair_kernel<MODE, GLU, F32>, &probe);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     *v = clusters < device_sm_count() / 2 ? clusters : device_sm_count() / 2;
@@ -673,7 +673,7 @@ cudaError_t run_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
   });
   if (err != cudaSuccess) return err;
   cfg.gridDim = dim3((unsigned)(2 * resident));
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE, GLU>, ta, tb, tc, p);
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE, GLU, F32>, ta, tb, tc, p);
 }
 
 }  // namespace
@@ -694,7 +694,7 @@ cudaError_t launch_linear_pair(int mode, const LinParams& base, const void* a, c
     if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, b, p.n_in, R, 64, 64);
     if (err == cudaSuccess) err = encode_tmap_3d_bf16(&tc, p.out, p.n_in, p.n_w, E, 64, 32);
     if (err != cudaSuccess) return err;
-    return run_pairs<kWgrad, false>(ta, tb, tc, p, st);
+    return run_pairs<kWgrad, false, false>(ta, tb, tc, p, st);
   }
   // a: rows of X or dZ, b: the weights; on pairs the weights are the A operand
   const uint64_t kc = mode == kFwd ? p.n_in : p.n_w;
@@ -707,8 +707,12 @@ cudaError_t launch_linear_pair(int mode, const LinParams& base, const void* a, c
   if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tb, a, kc, R, 64, 128);
   if (err == cudaSuccess) err = encode_tmap_2d_bf16(&tc, a, kc, R, 64, 64);
   if (err != cudaSuccess) return err;
-  if (mode == kDgrad) return run_pairs<kDgrad, false>(ta, tb, tc, p, st);
-  return glu ? run_pairs<kFwd, true>(ta, tb, tc, p, st) : run_pairs<kFwd, false>(ta, tb, tc, p, st);
+  if (mode == kDgrad) return run_pairs<kDgrad, false, false>(ta, tb, tc, p, st);
+  if (p.out32)
+    return glu ? run_pairs<kFwd, true, true>(ta, tb, tc, p, st)
+               : run_pairs<kFwd, false, true>(ta, tb, tc, p, st);
+  return glu ? run_pairs<kFwd, true, false>(ta, tb, tc, p, st)
+             : run_pairs<kFwd, false, false>(ta, tb, tc, p, st);
 }
 
 }  // namespace beam

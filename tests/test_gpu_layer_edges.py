@@ -191,3 +191,47 @@ def test_gradients_far_out(act):
         scale = (scale * z.double().chunk(2, -1)[1].abs().clamp(min=1)).repeat(1, 2)
     fine = (got == want) | ((got - want).abs() <= 2.0 ** -18 * terms + 2.0 ** -118 * scale)
     assert bool(fine.all()), list(zip(z[0].tolist(), got[0].tolist(), want[0].tolist()))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "swiglu"])
+@pytest.mark.parametrize("R,E,n_in,n_out", [(1, 1, 8, 64)] + SHAPES)
+def test_fp32_outputs_keep_fp32(R, E, n_in, n_out, act):
+    """One product a sum, so Z is exact and what is left is the activation's own error.
+
+    e^-z: 2^-22 from the exponential, 2^-24 from the product behind it; 1 + e 2^-24; the quotient
+    2^-22; swiglu's factor 2^-24: 3 2^-22 in all. gelu_tanh's argument 2a takes six roundings,
+    6 2^-24 |2a| of the gate. gelu: erfc within 2^-21, its argument's two roundings, which move
+    it by 2 2^-24 (1 + z^2) at most, and the product's. Below z = -80 (-9 gelu_tanh, -12 gelu) FP32 runs out: within
+    256 2^-126 of the other half there."""
+    N = n_out * (2 if act == "swiglu" else 1)
+    g = torch.Generator().manual_seed(R + n_out)
+    x, w = torch.zeros((R, n_in), dtype=BF), torch.zeros((E, N, n_in), dtype=BF)
+    x[:, 0] = (torch.randn(R, generator=g).exp()).to(BF)
+    w[:, :, 0] = (torch.randn((E, N), generator=g) * 12).to(BF)
+    lo = [min(R, e * (R // E + 1)) for e in range(E + 1)]
+    cfg = bm.linear_cfg(n_in, n_out, E, act, out_fp32=True)
+    y = torch.full((R, n_out), LEFT, device="cuda")
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R), dtype=torch.uint8, device="cuda")
+    bm.beam_moe_linear(cfg, x.cuda(), w.cuda(), y, ws,
+                       offsets=torch.tensor(lo, dtype=torch.int32, device="cuda"))
+    z = torch.cat([x[a:b, :1].double() * w[e, :, 0].double()
+                   for e, (a, b) in enumerate(zip(lo, lo[1:]))])
+    gate = z[:, :n_out]
+    if act == "gelu":
+        gate_of = 0.5 * torch.special.erfc(gate * -0.5 ** 0.5)
+    elif act == "gelu_tanh":
+        gate_of = torch.special.expit((8 / torch.pi) ** 0.5 * (gate + 0.044715 * gate ** 3))
+    else:
+        gate_of = torch.special.expit(gate)
+    other = z[:, n_out:] if act == "swiglu" else torch.ones_like(gate)
+    want = gate * gate_of * other
+    rel = {"gelu": 2.0 ** -21 + 2.0 ** -23 * (1 + gate ** 2) + 2.0 ** -24,
+           "gelu_tanh": 3 * 2.0 ** -22 + 6 * 2.0 ** -24 * (
+               (8 / torch.pi) ** 0.5 * (gate + 0.044715 * gate ** 3)).abs()
+           }.get(act, torch.full_like(gate, 3 * 2.0 ** -22))
+    deep = gate < {"gelu": -12, "gelu_tanh": -9}.get(act, -80)
+    tol = torch.where(deep, 2.0 ** -24 * want.abs(), rel * want.abs()) + (
+        2.0 ** -118 * other.abs().clamp(min=1))
+    tol = torch.where(deep, want.abs() + tol, tol)
+    err = (y.cpu().double() - want).abs()
+    assert bool((err <= tol).all()), (err / want.abs())[(err > tol)].max()
