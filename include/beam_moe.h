@@ -561,10 +561,13 @@ typedef struct beam_moe_linear_cfg {
 /*
  * Rows offsets[e] .. offsets[e+1]-1 through expert e:
  *   Z = X W_e^T + bias_e,  Y = act(Z) + residual.
- * Tensor-core products with FP32 accumulation (whose error grows with the
- * length of a sum, by up to 1.2e-9 of it per term: 3e-6 at n_in = 2560); bias,
- * activation and residual are added in FP32 before the one rounding. N is n_out, 2 n_out for swiglu
- * (weight rows 0..n_out-1 gate, n_out..2 n_out-1 up, as W13 of the block).
+ * Tensor-core products with FP32 accumulators, which cut off as they add: the
+ * error grows with a sum's length, per term by up to 6.8e-9 of the sum where
+ * all terms have one sign (3.5e-5 at n_in = 5120) and by up to 1e-9 of the sum
+ * of magnitudes else (5.6e-6 of the results' 2-norm there for terms around
+ * zero). Bias, activation and residual are added in FP32 before the one
+ * rounding. N is n_out, 2 n_out for swiglu (weight rows 0..n_out-1 gate,
+ * n_out..2 n_out-1 up, as W13 of the block).
  *   x        [rows][n_in], w [E][N][n_in], device
  *   bias     [E][N] fp32, residual [rows][n_out], or NULL
  *   offsets  [E+1] int32, device, ascending (beam_moe_permute's); NULL with
@@ -593,8 +596,8 @@ BEAM_MOE_API beam_moe_status beam_moe_linear(const beam_moe_linear_cfg* cfg, int
  *   dZ = dY act'(Z), dX = dZ W_e, dW_e = dZ^T X and dbias_e = sum dZ over the
  * rows of e (zero for an expert without rows). dZ is rounded to dtype once as
  * the products' operand; dbias sums it unrounded in FP32. dW's sums over an
- * expert's rows have the accumulators' error above: below fp16's half step up
- * to 2^18 rows of one expert, below bf16's up to 2^20.
+ * expert's rows leave the accumulators every 16384 rows and are added in FP32,
+ * so the accumulators' error above ends at 1.1e-4 of the sum of magnitudes.
  *   dy       [rows][n_out] of dtype; x, w, offsets as above
  *   z        [rows][N] of dtype, beam_moe_linear's; NULL only with act none
  *   dx       [rows][n_in], dw [E][N][n_in] of dtype, dbias [E][N] fp32 (out);

@@ -239,8 +239,10 @@ __device__ __forceinline__ void finish16(const LinParams& p, const Tile& t, int 
 
 // ------------------------------------------------------------------- kernel
 // bid: this CTA among those of the product. Split: consecutive groups of
-// p.parts CTAs share a tile each (a cluster holds one group or several).
-template <int MODE, int BN, bool SPLIT>
+// p.parts CTAs share a tile each (a cluster holds one group or several). LONG
+// (WGRAD): segments may be longer than a drain of the accumulators; the split form
+// without it is 0.4 us faster (300 x 640 x 640: 15.4 us).
+template <int MODE, int BN, bool SPLIT, bool LONG>
 __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                             const LinParams& p, int bid) {
   using C = LinCfg<BN, SPLIT>;
@@ -396,53 +398,54 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
       int ka, kb;
       k_range(t, ka, kb);
       if (ka == kb) continue;  // nothing to add: the epilogue takes zeros
-      if (!SPLIT) {
-        ok = warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-      for (int k = ka; k < kb; ++k) {
-        ok = warp_wait(&full[stage], phase, kFlagMma);
-        if (!ok) break;
-        int k16 = kK / 16;
-        if (MODE == kWgrad) {
-          const int rem = t.kcnt - k * kK;  // rows of the segment in this step
-          if (rem < kK) {
-            k16 = (rem + 15) / 16;
-            const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
-            for (int i = lane; i < dirty * 8 * (2 + BN / 64); i += 32) {
-              const int box = i / (dirty * 8), j = i - box * dirty * 8;
-              uint8_t* base = box < 2 ? smem + stage * a_stage + box * kBox
-                                      : ring_b + stage * C::kBBytes + (box - 2) * kBox;
-              reinterpret_cast<uint4*>(base)[rem * 8 + j] = make_uint4(0, 0, 0, 0);
+      for (int k0 = ka, k1; k0 < kb && ok; k0 = k1) {  // a drain each
+        k1 = LONG ? min(kb, k0 + kDrain) : kb;
+        if (!SPLIT || k0 != ka) {
+          ok = warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+        for (int k = k0; k < k1; ++k) {
+          ok = warp_wait(&full[stage], phase, kFlagMma);
+          if (!ok) break;
+          int k16 = kK / 16;
+          if (MODE == kWgrad) {
+            const int rem = t.kcnt - k * kK;  // rows of the segment in this step
+            if (rem < kK) {
+              k16 = (rem + 15) / 16;
+              const int dirty = k16 * 16 - rem;  // other rows inside the last MMA
+              for (int i = lane; i < dirty * 8 * (2 + BN / 64); i += 32) {
+                const int box = i / (dirty * 8), j = i - box * dirty * 8;
+                uint8_t* base = box < 2 ? smem + stage * a_stage + box * kBox
+                                        : ring_b + stage * C::kBBytes + (box - 2) * kBox;
+                reinterpret_cast<uint4*>(base)[rem * 8 + j] = make_uint4(0, 0, 0, 0);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+          }
+          tc_fence_after();
+          const uint64_t da = desc_a + (uint64_t)(stage * (a_stage >> 4));
+          const uint64_t db = desc_b + (uint64_t)(stage * (C::kBBytes >> 4));
+          if (one) {
+#pragma unroll
+            for (int q = 0; q < kK / 16; ++q)
+              if (MODE != kWgrad || q < k16)
+                umma_bf16(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != k0);
+            umma_commit(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        tc_fence_after();
-        const uint64_t da = desc_a + (uint64_t)(stage * (a_stage >> 4));
-        const uint64_t db = desc_b + (uint64_t)(stage * (C::kBBytes >> 4));
-        if (one) {
-#pragma unroll
-          for (int q = 0; q < kK / 16; ++q)
-            if (MODE != kWgrad || q < k16)
-              umma_bf16(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != ka);
-          umma_commit(&empty[stage]);
-        }
+        if (!ok) break;
+        if (one) umma_commit(&tfull[acc]);
         __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
-      if (one) umma_commit(&tfull[acc]);
-      __syncwarp();
-      if (!SPLIT) {
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        if (!SPLIT) acc ^= 1;
+        if (SPLIT || acc == 0) acc_phase ^= 1u;
       }
     }
     if (one) {
@@ -455,15 +458,35 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
     const int r = q * 32 + lane;
+    float* slot = p.sums + (int64_t)blockIdx.x * kSumFloats;  // WGRAD
     int acc = 0;
     uint32_t acc_phase = 0;
+    auto release = [&]() {  // the accumulator is read; on to the other one
+      tc_fence_before();
+      mbar_arrive(&tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    };
     for (int ti = first; ti < total; ti += step) {
       const Tile t = decode<MODE, BN>(ti, p, seg, bn_out);
       const bool none = t.nk == 0;
+      const int n_drains = LONG ? drains(t.nk) : 1;
+      bool ok = true;
+      for (int dr = 0; LONG && dr + 1 < n_drains; ++dr) {  // all but the last
+        ok = warp_wait(&tfull[acc], acc_phase, kFlagEpilogue);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c0 = 0; c0 < BN && t.n0 + c0 < p.cols; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN) + c0, v);
+          tmem_ld_wait();
+          add_drained(slot, c0, r, dr == 0, false, v);
+        }
+        release();
+      }
+      if (!ok) break;
       if (!none) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status,
-                                               kFlagEpilogue)))
-          break;
+        if (!warp_wait(&tfull[acc], acc_phase, kFlagEpilogue)) break;
         tc_fence_after();
       }
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
@@ -476,16 +499,12 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
           if (glu) tmem_ld16(tb + BN / 2 + c0, u);
           tmem_ld_wait();
         }
+        if (LONG && n_drains > 1) add_drained(slot, c0, r, false, true, a);
         if (r < t.rows)
           finish16<MODE>(p, t, r, t.n0 + c0, reinterpret_cast<float*>(a),
                          reinterpret_cast<const float*>(u));
       }
-      if (!none) {
-        tc_fence_before();
-        mbar_arrive(&tempty[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
-      }
+      if (!none) release();
     }
   }
 
@@ -516,18 +535,42 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
       }
       int ka, kb;
       k_range(t, ka, kb);
-      const bool got = ka < kb && warp_wait(&tfull[0], 0, kFlagEpilogue);
-      tc_fence_after();
-      for (int c0 = 0; c0 < BN; c0 += 16) {
-        uint32_t a[16];
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+      const int n_drains = LONG ? drains(kb - ka) : 1;
+      if (LONG && n_drains > 1) {
+        float sum[BN];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) a[j] = 0u;
-        if (got) {
-          tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c0, a);
-          tmem_ld_wait();
+        for (int j = 0; j < BN; ++j) sum[j] = 0.0f;
+        for (int dr = 0; dr < n_drains; ++dr) {
+          if (!warp_wait(&tfull[0], dr & 1, kFlagEpilogue)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < BN; c0 += 16) {
+            uint32_t a[16];
+            tmem_ld16(tb + c0, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c0 + j] += __uint_as_float(a[j]);
+          }
+          tc_fence_before();
+          mbar_arrive(&tempty[0]);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c0 + j) * kLd + r] = __uint_as_float(a[j]);
+        for (int j = 0; j < BN; ++j) part[j * kLd + r] = sum[j];
+      } else {
+        const bool got = ka < kb && warp_wait(&tfull[0], 0, kFlagEpilogue);
+        tc_fence_after();
+        for (int c0 = 0; c0 < BN; c0 += 16) {
+          uint32_t a[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) a[j] = 0u;
+          if (got) {
+            tmem_ld16(tb + c0, a);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[(c0 + j) * kLd + r] = __uint_as_float(a[j]);
+        }
       }
     }
     cluster_sync();
@@ -571,11 +614,11 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tm_a, const CUten
   }
 }
 
-template <int MODE, int BN, bool SPLIT>
+template <int MODE, int BN, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ LinParams p) {
-  linear_body<MODE, BN, SPLIT>(tm_a, tm_b, p, blockIdx.x);
+  linear_body<MODE, BN, SPLIT, LONG>(tm_a, tm_b, p, blockIdx.x);
 }
 
 // ------------------------------------------------------------- a few rows
@@ -920,6 +963,7 @@ struct Joint {
   float* dbias;
 };
 
+template <bool LONG>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_joint_kernel(const __grid_constant__ CUtensorMap dx_a,
                         const __grid_constant__ CUtensorMap dx_b,
@@ -927,9 +971,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const __grid_constant__ CUtensorMap dw_b, const __grid_constant__ Joint j) {
   const int b = blockIdx.x;
   if (b < j.dx_ctas) {
-    linear_body<kDgrad, 64, true>(dx_a, dx_b, j.dx, b);
+    linear_body<kDgrad, 64, true, false>(dx_a, dx_b, j.dx, b);
   } else if (b < j.dx_ctas + j.dw_ctas) {
-    linear_body<kWgrad, 64, true>(dw_a, dw_b, j.dw, b - j.dx_ctas);
+    linear_body<kWgrad, 64, true, LONG>(dw_a, dw_b, j.dw, b - j.dx_ctas);
   } else {
     const int i = b - j.dx_ctas - j.dw_ctas;
     if (i < j.join_x * j.join_y)
@@ -938,14 +982,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------------------------- launches
-template <int MODE, int BN, bool SPLIT>
+template <int MODE, int BN, bool SPLIT, bool LONG>
 cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p,
                          int64_t tiles, int parts, cudaStream_t st) {
   using C = LinCfg<BN, SPLIT>;
   static PerDevice configured;  // the shared-memory attribute, once per device
   int unused = 0;
   cudaError_t err = per_device(configured, &unused, [](int*) {
-    return cudaFuncSetAttribute(linear_kernel<MODE, BN, SPLIT>,
+    return cudaFuncSetAttribute(linear_kernel<MODE, BN, SPLIT, LONG>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   });
   if (err != cudaSuccess) return err;
@@ -962,7 +1006,7 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Lin
   cfg.numAttrs = SPLIT ? 1 : 0;
   const int64_t sms = device_sm_count();
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * parts : (tiles < sms ? tiles : sms)));
-  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BN, SPLIT>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BN, SPLIT, LONG>, ta, tb, p);
 }
 
 // dZ and the row blocks' sums of it. CTAs for about eight per SM walk the blocks.
@@ -1134,6 +1178,17 @@ cudaError_t set_up(const LinParams& base, const Choice& c, const void* a, const 
                                                   MODE == kDgrad ? 64 : (glu ? bn / 2 : bn));
 }
 
+template <int MODE, bool LONG>
+cudaError_t launch_form(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p,
+                        const Choice& c, int64_t tiles, cudaStream_t st) {
+  if (c.bn == 256) return launch_tiles<MODE, 256, false, LONG>(ta, tb, p, tiles, 1, st);
+  if (c.bn == 128) return launch_tiles<MODE, 128, false, LONG>(ta, tb, p, tiles, 1, st);
+  return launch_tiles<MODE, 64, true, LONG>(ta, tb, p, tiles, c.parts, st);
+}
+
+// Whether an expert's rows may be more than a drain of the accumulators takes.
+bool long_sums(int64_t rows) { return rows > (int64_t)kDrain * kK; }
+
 template <int MODE>
 cudaError_t launch_product(const LinParams& base, const Choice& c, const void* a, const void* b,
                            cudaStream_t st) {
@@ -1149,9 +1204,9 @@ cudaError_t launch_product(const LinParams& base, const Choice& c, const void* a
   int64_t tiles;
   const cudaError_t err = set_up<MODE>(base, c, a, b, &p, &ta, &tb, &tiles);
   if (err != cudaSuccess) return err;
-  if (c.bn == 256) return launch_tiles<MODE, 256, false>(ta, tb, p, tiles, 1, st);
-  if (c.bn == 128) return launch_tiles<MODE, 128, false>(ta, tb, p, tiles, 1, st);
-  return launch_tiles<MODE, 64, true>(ta, tb, p, tiles, c.parts, st);
+  if (MODE == kWgrad && long_sums(p.rows))
+    return launch_form<MODE, MODE == kWgrad>(ta, tb, p, c, tiles, st);
+  return launch_form<MODE, false>(ta, tb, p, c, tiles, st);
 }
 
 int64_t split_ctas(int mode, const LinParams& p, const Choice& c) {
@@ -1182,6 +1237,7 @@ bool choose_backward(const LinParams& p, int block, Choice* dx, Choice* dw) {
   return true;
 }
 
+template <bool LONG>
 cudaError_t launch_joint(const LinParams& base, const Choice& cx, const Choice& cw, const void* dz,
                          const void* x, const void* w, void* dx, void* dw, const float* part,
                          float* dbias, cudaStream_t st) {
@@ -1208,8 +1264,8 @@ cudaError_t launch_joint(const LinParams& base, const Choice& cx, const Choice& 
   static PerDevice configured;
   int unused = 0;
   err = per_device(configured, &unused, [](int*) {
-    return cudaFuncSetAttribute(linear_joint_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                C::kSmemBytes);
+    return cudaFuncSetAttribute(linear_joint_kernel<LONG>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   });
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -1224,11 +1280,11 @@ cudaError_t launch_joint(const LinParams& base, const Choice& cx, const Choice& 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(j.dx_ctas + j.dw_ctas + whole((int64_t)j.join_x * j.join_y)));
-  return cudaLaunchKernelEx(&cfg, linear_joint_kernel, xa, xb, wa, wb, j);
+  return cudaLaunchKernelEx(&cfg, linear_joint_kernel<LONG>, xa, xb, wa, wb, j);
 }
 
 struct LinLayout {
-  size_t part, dz, total;
+  size_t part, dz, sums, total;
   int block;       // rows per block of the dZ kernel
   int64_t blocks;  // row blocks at most
 };
@@ -1258,11 +1314,14 @@ LinLayout lin_layout(const beam_moe_linear_cfg& c, int64_t rows, bool backward) 
     room = most_blocks(wide_from - 1, E, 32);
   L.part = 256;
   L.dz = L.part;
+  L.sums = L.dz;
   L.total = 256;
   if (backward) {
     const size_t n_w = (size_t)weight_rows(c);
     L.dz = (L.part + (size_t)room * n_w * 4 + 1023) / 1024 * 1024;
-    L.total = L.dz + (c.act == BEAM_MOE_ACT_NONE ? 0 : ((size_t)rows * n_w * 2 + 255) / 256 * 256);
+    L.sums = L.dz + (c.act == BEAM_MOE_ACT_NONE ? 0 : ((size_t)rows * n_w * 2 + 255) / 256 * 256);
+    L.total = L.sums;
+    if (long_sums(rows)) L.total += (size_t)device_sm_count() * kSumFloats * 4;
   }
   return L;
 }
@@ -1275,9 +1334,7 @@ beam_moe_status check_linear(const beam_moe_linear_cfg* c, int64_t rows) {
   if (c->out_fp32 != 0 && c->out_fp32 != 1) return BEAM_MOE_ERR_INVALID_ARG;
   if (c->n_in % 8 || c->n_out % 8 || c->n_in > 65536 || c->n_out > 65536 || c->n_experts > kMaxE)
     return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
-  // dW sums an expert's rows in the tensor cores' FP32 accumulators, which lose up
-  // to 1.2e-9 of the sum per row: 5e-3, a bf16 step, at 2^22 rows of one
-  // expert (9e-4 measured there; 30 ms, inside one bounded wait)
+  // (2^22 rows of one expert through one tile: 30 ms, well inside the bounded waits)
   if (rows > (int64_t)1 << 22) return BEAM_MOE_ERR_UNSUPPORTED_SHAPE;
   return BEAM_MOE_OK;
 }
@@ -1401,7 +1458,8 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
   beam::Choice cx, cw;
   const bool joint = beam::choose_backward(p, L.block, &cx, &cw);
   if (joint && dx && dw) {
-    LIN_CUDA(beam::launch_joint(p, cx, cw, dz, x, w, dx, dw, part, dbias, st));
+    LIN_CUDA((beam::long_sums(rows) ? beam::launch_joint<true> : beam::launch_joint<false>)(
+        p, cx, cw, dz, x, w, dx, dw, part, dbias, st));
     return BEAM_MOE_OK;
   }
   if (dbias) LIN_CUDA(beam::launch_bias_join(p, part, L.block, dbias, st));
@@ -1412,6 +1470,7 @@ beam_moe_status beam_moe_linear_backward(const beam_moe_linear_cfg* cfg, int64_t
   }
   if (dw) {
     p.out = dw;
+    p.sums = reinterpret_cast<float*>(base + L.sums);
     LIN_CUDA(beam::launch_product<beam::kWgrad>(p, cw, dz, x, st));
   }
   return BEAM_MOE_OK;

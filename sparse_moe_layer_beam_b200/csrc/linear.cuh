@@ -38,7 +38,35 @@ struct LinParams {
   unsigned* status;
   int clear_status;        // the launch clears the status area (the first of a call)
   int* next_tile;          // CTA pairs: counter of the tiles handed out
+  float* sums;             // WGRAD: kSumFloats per CTA, where rows > kDrain kK
 };
+
+// The tensor cores cut off as they add to an FP32 accumulator, so a sum whose
+// terms have one sign comes out too small by up to 6.8e-9 of itself per term
+// (measured; terms of both signs 1e-9 and less): fp16's half step, 2^-11, at 72,000
+// rows. dW's sums over rows are therefore taken out of the accumulators every 256
+// steps (16384 rows, 1.1e-4) and added in FP32: one-CTA tiles and pairs in a slot
+// of the workspace per CTA, while the other accumulator fills; split tiles in
+// registers. 65536 x 2560 x 2560, both products: 1288 us without, 1296 every 512
+// steps, 1313 every 128, 1330 every 64.
+constexpr int kDrain = 256;            // contraction steps
+constexpr int kSumFloats = 128 * 256;  // a CTA's accumulator
+
+__device__ __forceinline__ int drains(int steps) { return (steps + kDrain - 1) / kDrain; }
+
+// v (column c on, row r of the CTA's accumulator) with what the earlier drains
+// of the tile left there; kept there unless this one is the last.
+__device__ __forceinline__ void add_drained(float* slot, int c, int r, bool first, bool last,
+                                            uint32_t (&v)[16]) {
+  float* s = slot + c * kM + r;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float f = __uint_as_float(v[j]);
+    if (!first) f += s[j * kM];
+    if (last) v[j] = __float_as_uint(f);
+    else s[j * kM] = f;
+  }
+}
 
 constexpr int kStatusWords = 64;
 
@@ -229,15 +257,14 @@ __device__ __forceinline__ uint32_t idesc_of(bool fp16, bool a_mn, bool b_mn, ui
 }
 
 // ----------------------------------------------------------------- epilogue
-// e^-z. __expf rounds z log2(e) before it raises 2 to it, so its error grows with
-// |z|: 25 steps at z = -20. That is far below a half step of a 16-bit result,
-// where it is used (FULL false). FULL, for FP32 results and where a row or two
-// cost nothing, puts the rounding back (Cody
-// and Waite's two-part ln 2): with t = fl(-z log2 e), e^-z = 2^t e^(-z - t ln 2), and the second factor is
-// 1 + r to first order (r < 1e-5). Used for all results it cost 5 % where a
-// short contraction leaves the epilogue as the bound (16384 x 512 x 5120, swiglu:
-// 243 and 256 us); expf and a full division there 449 us. z is held to +-88,
-// beyond which the quotients below are 0 and 1 either way.
+// e^-z. __expf is documented to err by 2 + 1.17 |z| steps: 25 at z = -20. That is
+// far below a half step of a 16-bit result, where it is used (FULL false). FULL is
+// for FP32 results, and for forms that finish few values: with t the FP32 nearest
+// to -z log2 e, e^-z = 2^t e^r, r = -z - t ln 2 (ln 2 in two parts, after Cody and
+// Waite), and e^r is 1 + r to first order (r < 1e-5). Used for all results it cost
+// 5 % where a short contraction leaves the epilogue as the bound (16384 x 512 x
+// 5120, swiglu: 243 and 256 us); expf and a full division there 449 us. z is held
+// to +-88, beyond which the quotients below are 0 and 1 either way.
 template <bool FULL>
 __device__ __forceinline__ float exp_neg(float z) {
   if (!FULL) return __expf(-z);

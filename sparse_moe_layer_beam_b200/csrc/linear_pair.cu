@@ -449,37 +449,41 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
         const uint32_t idesc =
             idesc_of(p.fp16, MODE != kFwd, MODE == kWgrad, kPair,
                      MODE == kWgrad ? kPair : (uint32_t)((t.rows + 15) & ~15));
-        if (!warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma, false)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * kPair);
-        for (int k = 0; k < t.nk; ++k) {
-          // WGRAD: the other CTA's cleaned rows come with its arrival
-          if (!warp_wait(&full[stage], phase, kFlagMma, MODE == kWgrad)) {
-            ok = false;
-            break;
-          }
+        for (int k0 = 0, k1; k0 < t.nk && ok; k0 = k1) {  // a drain each
+          k1 = MODE == kWgrad ? min(t.nk, k0 + kDrain) : t.nk;
+          ok = warp_wait(&tempty[acc], acc_phase ^ 1u, kFlagMma, false);
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t da = desc_a + (uint64_t)(stage * (kStageBytes >> 4));
-          const uint64_t db = desc_b + (uint64_t)(stage * (kStageBytes >> 4));
-          const int k16 = MODE == kWgrad ? min(kK / 16, (t.rows - k * kK + 15) / 16) : kK / 16;
-          if (one) {
+          const uint32_t d = tmem_base + (uint32_t)(acc * kPair);
+          for (int k = k0; k < k1; ++k) {
+            // WGRAD: the other CTA's cleaned rows come with its arrival
+            if (!warp_wait(&full[stage], phase, kFlagMma, MODE == kWgrad)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t da = desc_a + (uint64_t)(stage * (kStageBytes >> 4));
+            const uint64_t db = desc_b + (uint64_t)(stage * (kStageBytes >> 4));
+            const int k16 = MODE == kWgrad ? min(kK / 16, (t.rows - k * kK + 15) / 16) : kK / 16;
+            if (one) {
 #pragma unroll
-            for (int q = 0; q < kK / 16; ++q)
-              if (MODE != kWgrad || q < k16)
-                umma_bf16_pair(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != 0);
-            umma_commit_pair(&empty[stage], 0x3);
+              for (int q = 0; q < kK / 16; ++q)
+                if (MODE != kWgrad || q < k16)
+                  umma_bf16_pair(d, da + kStepA * q, db + kStepB * q, idesc, q ? 1u : k != k0);
+              umma_commit_pair(&empty[stage], 0x3);
+            }
+            __syncwarp();
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (!ok) break;
+          if (one) umma_commit_pair(&tfull[acc], 0x3);
           __syncwarp();
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        if (one) umma_commit_pair(&tfull[acc], 0x3);
-        __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
       // Every MMA of the pair completes before TMEM is released.
       if (one) {
@@ -518,15 +522,35 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     int acc = 0;
     uint32_t acc_phase = 0;
+    float* slot = p.sums + (int64_t)blockIdx.x * kSumFloats;  // WGRAD
+    auto release = [&]() {  // the accumulator is read; on to the other one
+      tc_fence_before();
+      mbar_arrive_cluster(mapa_shared(smem_addr(&tempty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    };
     int staged = 0;  // WGRAD: the staging block in turn
     for (;;) {
       const PairTile t = read_tile(kFlagEpilogue);
       if (t.e < 0) break;
       const bool none = t.nk == 0;
+      const int n_drains = MODE == kWgrad ? drains(t.nk) : 1;
+      bool ok = true;
+      for (int dr = 0; MODE == kWgrad && dr + 1 < n_drains; ++dr) {  // all but the last
+        ok = warp_wait(&tfull[acc], acc_phase, kFlagEpilogue, false);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c0 = 0; c0 < kPair && t.n0 + c0 < p.n_in; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kPair) + c0, v);
+          tmem_ld_wait();
+          add_drained(slot, c0, q * 32 + lane, dr == 0, false, v);
+        }
+        release();
+      }
+      if (!ok) break;
       if (!none) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status,
-                                               kFlagEpilogue)))
-          break;
+        if (!warp_wait(&tfull[acc], acc_phase, kFlagEpilogue, false)) break;
         tc_fence_after();
       }
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kPair);
@@ -549,6 +573,11 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
             }
           }
           if (!none) tmem_ld_wait();
+          if (n_drains > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              add_drained(slot, c0 + i * 16, q * 32 + lane, false, true, v[i]);
+          }
           // the store before the last has read its block
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           __syncwarp();
@@ -621,12 +650,7 @@ __global__ void __launch_bounds__(PairMem<MODE>::kBlock, 1)
           }
         }
       }
-      if (!none) {
-        tc_fence_before();
-        mbar_arrive_cluster(mapa_shared(smem_addr(&tempty[acc]), 0));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
-      }
+      if (!none) release();
     }
     if (MODE == kWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }

@@ -235,3 +235,62 @@ def test_fp32_outputs_keep_fp32(R, E, n_in, n_out, act):
     tol = torch.where(deep, want.abs() + tol, tol)
     err = (y.cpu().double() - want).abs()
     assert bool((err <= tol).all()), (err / want.abs())[(err > tol)].max()
+
+
+# rows, offsets, n_in, n_out: tiles split over a cluster; 128- and 256-column tiles; CTA pairs; a
+# dense layer, and experts whose segments end inside a step
+LONG = [(1 << 20, None, 64, 64), ((1 << 20) + 37, (0, 5, 40_000, (1 << 20) + 30), 72, 136),
+        ((1 << 20) + 5, None, 1024, 1024), ((1 << 19) + 3, None, 4096, 1152),
+        ((1 << 19) + 77, (0, 32_769, 32_769, (1 << 19) + 70), 1032, 2600)]
+
+
+@pytest.mark.parametrize("R,off,n_in,n_out", LONG)
+def test_long_sums_of_one_sign(R, off, n_in, n_out):
+    """dW over half a million rows and more, fp16, every term positive: half a step, 2^-11; what
+    the tensor cores cut off, at most a step of the sum, 2^-23, for each 16 of the 16384 rows
+    between drains; and one FP32 addition a drain."""
+    E = len(off) - 1 if off else 1
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = (0.5 + torch.rand((R, n_in), generator=g, device="cuda", dtype=torch.float16))
+    dy = (0.5 + torch.rand((R, n_out), generator=g, device="cuda", dtype=torch.float16)) * 2.0 ** -10
+    cfg = bm.linear_cfg(n_in, n_out, E, dtype="fp16")
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R, True), dtype=torch.uint8,
+                     device="cuda")
+    dw = torch.full((E, n_out, n_in), LEFT, dtype=torch.float16, device="cuda")
+    bm.beam_moe_linear_backward(
+        cfg, dy, x, None, ws, dw=dw,
+        offsets=torch.tensor(off, dtype=torch.int32, device="cuda") if off else None)
+    assert bm.beam_moe_check(ws) == 0
+    for e, (a, b) in enumerate(zip(off or (0,), off[1:] if off else (R,))):
+        want = torch.zeros((n_out, n_in), dtype=torch.float64, device="cuda")
+        for i in range(a, b, 1 << 16):
+            j = min(b, i + (1 << 16))
+            want += dy[i:j].double().T @ x[i:j].double()
+        err = (dw[e].double() - want).abs()
+        tol = (2.0 ** -11 + 1024 * 2.0 ** -23 + (R >> 14) * 2.0 ** -24) * want
+        assert bool((err <= tol).all()), (e, (err / want).max().item())
+
+
+@pytest.mark.parametrize("off", [None, (0, 3, 20_003, 49_990)])
+def test_long_sums_beside_the_other_gradients(off):
+    """All three gradients of 50000 narrow rows: both products and the biases' sums in one launch,
+    dW's sums drained on the way. Whole numbers: exact."""
+    R, n_in, n_out = 50_000, 64, 72
+    E = len(off) - 1 if off else 1
+    x, w, dy = whole((R, n_in), 1), whole((E, n_out, n_in), 2), whole((R, n_out), 3)
+    cfg = bm.linear_cfg(n_in, n_out, E)
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R, True), dtype=torch.uint8,
+                     device="cuda")
+    dx = torch.full((R, n_in), LEFT, dtype=BF, device="cuda")
+    dw = torch.full((E, n_out, n_in), LEFT, dtype=BF, device="cuda")
+    db = torch.full((E, n_out), LEFT, device="cuda")
+    bm.beam_moe_linear_backward(
+        cfg, dy.cuda(), x.cuda(), w.cuda(), ws, dx=dx, dw=dw, dbias=db,
+        offsets=torch.tensor(off, dtype=torch.int32, device="cuda") if off else None)
+    assert bm.beam_moe_check(ws) == 0
+    wdx = torch.full((R, n_in), LEFT, dtype=BF)
+    for e, (a, b) in enumerate(zip(off or (0,), off[1:] if off else (R,))):
+        wdx[a:b] = (dy[a:b].float() @ w[e].float()).to(BF)
+        assert torch.equal(dw[e].cpu(), (dy[a:b].float().T @ x[a:b].float()).to(BF))
+        assert torch.equal(db[e].cpu(), dy[a:b].float().sum(0))
+    assert torch.equal(dx.cpu(), wdx)
