@@ -294,3 +294,95 @@ def test_long_sums_beside_the_other_gradients(off):
         assert torch.equal(dw[e].cpu(), (dy[a:b].float().T @ x[a:b].float()).to(BF))
         assert torch.equal(db[e].cpu(), dy[a:b].float().sum(0))
     assert torch.equal(dx.cpu(), wdx)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "swiglu"])
+def test_each_bias_gradient_is_its_difference(act):
+    """Every element of dbias against the central difference of its own column's loss, step
+    h = 2^-6. Z is whole numbers and quarters below 64, which bf16 holds exactly, so the backward
+    sees the forward's Z. A difference is off by h^2/6 max|act'''| of the sum of |dY| (silu''' and
+    gelu''' below 0.8; swiglu 0.5 |up|, as the other half stands still) and by 2^-20 (|Z| + |Y|) / h
+    of |dY| for the two outputs' errors; dbias itself by 2^-18 of its terms."""
+    counts, n_in, n_out, h = [40, 0, 90], 64, 72, 2.0 ** -6
+    R, E, N = sum(counts), len(counts), n_out * (2 if act == "swiglu" else 1)
+    x, w = whole((R, n_in), 1), whole((E, N, n_in), 2)
+    bias = (torch.randint(0, 4, (E, N), generator=torch.Generator().manual_seed(3)) + 0.5) / 4
+    if act != "relu":  # relu: an eighth keeps Z away from the corner
+        bias = bias - 0.125
+    dy = torch.randn((R, n_out), generator=torch.Generator().manual_seed(4)).to(BF)
+    off = torch.tensor([0, 40, 40, 130], dtype=torch.int32, device="cuda")
+    cfg, wide = bm.linear_cfg(n_in, n_out, E, act), bm.linear_cfg(n_in, n_out, E, act, out_fp32=True)
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R, True), dtype=torch.uint8,
+                     device="cuda")
+    xd, wd = x.cuda(), w.cuda()
+
+    def forward(b):
+        y = torch.empty((R, n_out), device="cuda")
+        z = torch.empty((R, N), dtype=BF, device="cuda")
+        bm.beam_moe_linear(wide, xd, wd, y, ws, bias=b.cuda(), offsets=off, z=z)
+        return y.cpu().double(), z
+
+    y, zd = forward(bias)
+    db = torch.empty((E, N), device="cuda")
+    bm.beam_moe_linear_backward(cfg, dy.cuda(), None, None, ws, dbias=db, offsets=off,
+                                z=None if act == "none" else zd)
+    z, dyd, db = zd.cpu().double(), dy.double(), db.cpu().double()
+    terms = ref.act_grad_terms(dyd, z, act).abs()
+    for half in range(N // n_out):
+        step = torch.zeros((E, N))
+        step[:, half * n_out:(half + 1) * n_out] = h
+        diff = (forward(bias + step)[0] - forward(bias - step)[0]) / (2 * h) * dyd
+        third = 0.0 if act in ("none", "relu") else 0.8
+        if act == "swiglu":
+            third = 0.5 * z[:, n_out:].abs() if half == 0 else 0.0
+        each = dyd.abs() * (h * h / 6 * third
+                            + 2.0 ** -20 * (z.abs().reshape(R, -1, n_out).amax(1) + y.abs() + 1) / h)
+        for e, (a, b) in enumerate(((0, 40), (40, 40), (40, 130))):
+            cols = slice(half * n_out, (half + 1) * n_out)
+            tol = each[a:b].sum(0) + 2.0 ** -18 * terms[a:b, cols].sum(0)
+            assert bool(((diff[a:b].sum(0) - db[e, cols]).abs() <= tol).all()), (act, half, e)
+
+
+@pytest.mark.parametrize("R", [2, 9, 64, 512, 3000])
+def test_many_experts_at_full_width(R):
+    """A batch over 256 experts of the block's own width, 5120 -> 2 x 2560 and back, decode to a
+    small prefill: one row an expert or none, and a few. x has one value per row and 64 columns,
+    so that Z is exact (a product of two bf16 numbers sums to one term per row) and each row shows
+    which weights it met."""
+    E, H, I = 256, 5120, 2560
+    g = torch.Generator(device="cuda").manual_seed(R)
+    w = (torch.randint(1, 128, (E, 2 * I, 1), generator=g, device="cuda").float() / 64).to(BF)
+    w13 = w * torch.ones((1, 1, H), device="cuda", dtype=BF)
+    pick = torch.randint(0, E, (R,), generator=g, device="cuda").sort().values
+    off = torch.searchsorted(pick, torch.arange(E + 1, device="cuda")).int()
+    x = torch.zeros((R, H), dtype=BF, device="cuda")
+    at = torch.randint(0, H, (R,), generator=g, device="cuda")
+    v = (torch.randint(-64, 65, (R,), generator=g, device="cuda").float() / 16).to(BF)
+    x[torch.arange(R), at] = v
+    cfg = bm.linear_cfg(H, I, E, "swiglu")
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R, True), dtype=torch.uint8,
+                     device="cuda")
+    h = torch.full((R, I), LEFT, dtype=BF, device="cuda")
+    z = torch.full((R, 2 * I), LEFT, dtype=BF, device="cuda")
+    bm.beam_moe_linear(cfg, x, w13, h, ws, offsets=off, z=z)
+    assert bm.beam_moe_check(ws) == 0
+    want = v.double()[:, None] * w[pick, :, 0].double()
+    assert torch.equal(z, want.to(BF))
+    act = ref.act(want, "swiglu")
+    # half a step, and 2^-18 for the FP32 arithmetic before it
+    assert bool(((h.double() - act).abs() <= (2.0 ** -8 + 2.0 ** -18) * act.abs()).all())
+    # dX: one row of W_e at a time comes back; dW: every expert's own outer products
+    dz = torch.zeros((R, 2 * I), dtype=BF, device="cuda")
+    col = torch.randint(0, 2 * I, (R,), generator=g, device="cuda")
+    dz[torch.arange(R), col] = 2.0
+    plain = bm.linear_cfg(H, 2 * I, E)
+    dx = torch.full((R, H), LEFT, dtype=BF, device="cuda")
+    dw = torch.full((E, 2 * I, H), LEFT, dtype=BF, device="cuda")
+    ws = torch.empty(bm.beam_moe_linear_workspace_size(plain, R, True), dtype=torch.uint8,
+                     device="cuda")
+    bm.beam_moe_linear_backward(plain, dz, x, w13, ws, dx=dx, dw=dw, offsets=off)
+    assert bm.beam_moe_check(ws) == 0
+    assert torch.equal(dx, (2 * w13[pick, col].float()).to(BF))
+    wdw = torch.zeros((E, 2 * I, H), dtype=torch.float32, device="cuda")
+    wdw.index_put_((pick, col, at), 2 * v.float(), accumulate=True)
+    assert torch.equal(dw, wdw.to(BF))
