@@ -463,7 +463,8 @@ BEAM_MOE_API beam_moe_status beam_moe_ep_release(const beam_moe_ep_handle* handl
  * the routes beam_moe_route or a routing replay gives. A layer is
  *   permute -> linear (swiglu, W13) -> linear (W2) -> combine
  * and its backward the four backward calls in reverse. The conventions at the
- * top of this file hold; rows may be of any width unless stated.
+ * top of this file hold; rows may be of any width unless stated. Outputs must
+ * not overlap inputs or one another unless a call says that they may.
  */
 typedef enum beam_moe_dtype {
   BEAM_MOE_BF16 = 0,

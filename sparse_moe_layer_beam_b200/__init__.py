@@ -411,7 +411,15 @@ def _begin(name, t):
         _bind_torch()
     if not t.is_cuda or t.get_device() != _device():
         raise ValueError(f"{name}: not on the current CUDA device")
+    _rows(name, t)
     return t.get_device()
+
+
+def _rows(name, t):
+    """The first dimension of a tensor that is required."""
+    if t is None or not t.dim():
+        raise ValueError(f"{name}: a tensor of two dimensions is required")
+    return t.shape[0]
 
 
 def _tensor(name, t, kind, dev, shape):
@@ -474,7 +482,7 @@ def beam_moe_permute(cfg, x, topk_ids, xp, pos, offsets, ws, stream=None):
 def beam_moe_permute_backward(cfg, dxp, pos, dx, stream=None):
     """dx[t] = sum_k dxp[pos[t, k]]: dxp [rows, H], pos [T, K] -> dx [T, H]."""
     dev = _begin("dx", dx)
-    T, rows, H, d = dx.shape[0], _need("dxp", dxp).shape[0], cfg.width, cfg.dtype
+    T, rows, H, d = dx.shape[0], _rows("dxp", dxp), cfg.width, cfg.dtype
     _check(lib().beam_moe_permute_backward(
         cfg, T, rows, _tensor("dxp", dxp, d, dev, (rows, H)),
         _tensor("pos", _need("pos", pos), _I32, dev, (T, cfg.top_k)),
@@ -490,7 +498,7 @@ def beam_moe_combine(cfg, y, pos, w, out, stream=None):
     """out[t] = sum_k w[t, k] y[pos[t, k]]: y [rows, H] of cfg's dtype or fp32,
     w [T, K] fp32 or None (ones) -> out [T, H]."""
     dev = _begin("out", out)
-    T, rows, H, K = out.shape[0], _need("y", y).shape[0], cfg.width, cfg.top_k
+    T, rows, H, K = out.shape[0], _rows("y", y), cfg.width, cfg.top_k
     kind = _y_kind(cfg, y)
     _check(lib().beam_moe_combine(
         cfg, T, rows, _tensor("y", y, kind, dev, (rows, H)), kind,
@@ -502,8 +510,8 @@ def beam_moe_combine_backward(cfg, dout, y, pos, w, dy, dw, stream=None):
     """dy[pos[t, k]] = w[t, k] dout[t] (dy as y, or None), dw[t, k] =
     <dout[t], y[pos[t, k]]> (fp32 [T, K], or None; y may be None without it)."""
     dev = _begin("dout", dout)
-    like = y if y is not None else _need("dy", dy)
-    T, rows, H, K = dout.shape[0], like.shape[0], cfg.width, cfg.top_k
+    like = y if y is not None else dy
+    T, rows, H, K = dout.shape[0], _rows("y or dy", like), cfg.width, cfg.top_k
     kind = _y_kind(cfg, like)
     _check(lib().beam_moe_combine_backward(
         cfg, T, rows, _tensor("dout", dout, cfg.dtype, dev, (T, H)),

@@ -386,3 +386,25 @@ def test_many_experts_at_full_width(R):
     wdw = torch.zeros((E, 2 * I, H), dtype=torch.float32, device="cuda")
     wdw.index_put_((pick, col, at), 2 * v.float(), accumulate=True)
     assert torch.equal(dw, wdw.to(BF))
+
+
+def test_tensors_without_a_dimension_are_refused():
+    c, lc = bm.rows_cfg(16, 4, 2), bm.linear_cfg(16, 8)
+    bad = torch.zeros((), dtype=BF, device="cuda")
+    x = torch.zeros((3, 16), dtype=BF, device="cuda")
+    pos = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    w = torch.zeros((1, 8, 16), dtype=BF, device="cuda")
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    for call in (lambda: bm.beam_moe_permute(c, bad, pos, x, pos, off, ws),
+                 lambda: bm.beam_moe_permute_backward(c, bad, pos, x),
+                 lambda: bm.beam_moe_permute_backward(c, x, pos, bad),
+                 lambda: bm.beam_moe_permute_backward(c, None, pos, x),
+                 lambda: bm.beam_moe_combine(c, bad, pos, None, x),
+                 lambda: bm.beam_moe_combine(c, x, pos, None, bad),
+                 lambda: bm.beam_moe_combine_backward(c, x, bad, pos, None, x, None),
+                 lambda: bm.beam_moe_combine_backward(c, x, None, pos, None, None, None),
+                 lambda: bm.beam_moe_linear(lc, bad, w, x, ws),
+                 lambda: bm.beam_moe_linear_backward(lc, bad, x, w, ws, dx=x)):
+        with pytest.raises(ValueError):
+            call()
