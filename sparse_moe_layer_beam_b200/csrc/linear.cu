@@ -1098,8 +1098,9 @@ Choice choose(int mode, const LinParams& p, bool glu) {
   const double out = dw ? 3.0 : 0.0;  // dW's stores, which few steps do not hide
   consider(128, turns(tiles(128, 128), sms) * (steps * 0.27 + out) + 9.0);
   consider(256, turns(tiles(128, 256), sms) * (steps * 0.48 + 2 * out) + 12.0);
-  // experts with few rows stream their weights: one CTA per tile does that at
-  // the copy bandwidth, a pair at 0.9 of it
+  // Experts with few rows stream their weights, at the copy bandwidth in either
+  // form: 512 rows over 256 experts, 5120 -> 2 x 2560, 1640 us on one CTA a tile
+  // and 1615 on pairs, 64 rows 439 and 453, 512 rows 2560 -> 5120 785 and 798.
   if (dw || R / E >= 96) {
     const double t = dw ? tiles(256, 256) : row_blocks(256) * up(p.cols, glu ? 128 : 256);
     consider(0, turns(t, sms / 2) * (steps * 0.40 + 0.7 * out) + 8.0);
