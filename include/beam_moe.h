@@ -531,7 +531,7 @@ BEAM_MOE_API beam_moe_status beam_moe_combine(const beam_moe_rows_cfg* cfg, int6
  *   dout [T][H] of cfg->dtype; y, pos, w as for beam_moe_combine
  *   dy   [rows][H] of y_dtype (out), or NULL; rows that no slot names are left
  *        as they were; no two slots may name the same row (permute's do not)
- *   dw   [T][K] fp32 (out), or NULL; y may be NULL without it
+ *   dw   [T][K] fp32 (out), or NULL; without it y may be NULL, or dy's buffer
  */
 BEAM_MOE_API beam_moe_status beam_moe_combine_backward(const beam_moe_rows_cfg* cfg, int64_t T,
                                                        int64_t rows, const void* dout,
@@ -564,8 +564,8 @@ typedef struct beam_moe_linear_cfg {
  *   Z = X W_e^T + bias_e,  Y = act(Z) + residual.
  * Tensor-core products with FP32 accumulators, which cut off as they add: the
  * error grows with a sum's length, per term by up to 6.8e-9 of the sum where
- * all terms have one sign (3.5e-5 at n_in = 5120) and by up to 1e-9 of the sum
- * of magnitudes else (5.6e-6 of the results' 2-norm there for terms around
+ * all terms have one sign (3.5e-5 at n_in = 5120) and by up to 1.6e-9 of the
+ * sum of magnitudes else (6e-6 of the results' 2-norm there for terms around
  * zero). Bias, activation and residual are added in FP32 before the one
  * rounding. N is n_out, 2 n_out for swiglu (weight rows 0..n_out-1 gate,
  * n_out..2 n_out-1 up, as W13 of the block).

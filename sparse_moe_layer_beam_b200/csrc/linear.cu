@@ -638,9 +638,10 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
 // CUDA cores, two weight rows a warp, FP32 FMAs against X in shared memory, the
 // next weights' loads in flight meanwhile; lanes' sums are added by a
 // shuffle tree. RT rows of a dense layer share the weights; with experts
-// (RT = 1) blockIdx.y is the row. Bound by HBM: one token through 5120 x 5120
-// 11.8 us, 4.4 TB/s, a call's fixed part included (tensor cores 17.3 us); four
-// rows of four experts, swiglu, 41 us (58). One weight row a warp with twice
+// (RT = 1) blockIdx.y is the row. One token through 5120 x 5120 11.4 us, 4.6 TB/s,
+// a call's fixed part included (tensor cores 17.3 us): bound by the fullest SM of
+// one uneven wave (640 CTAs: 5 where the mean is 4.3). Four rows of four experts,
+// swiglu, 41 us (58). One weight row a warp with twice
 // the loads 13.3 us, four vectors per turn 14.8.
 template <int RT, bool GLU>
 __global__ void __launch_bounds__(kFewThreads)

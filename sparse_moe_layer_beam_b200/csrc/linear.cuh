@@ -43,12 +43,12 @@ struct LinParams {
 
 // The tensor cores cut off as they add to an FP32 accumulator, so a sum whose
 // terms have one sign comes out too small by up to 6.8e-9 of itself per term
-// (measured; terms of both signs 1e-9 and less): fp16's half step, 2^-11, at 72,000
-// rows. dW's sums over rows are therefore taken out of the accumulators every 256
-// steps (16384 rows, 1.1e-4) and added in FP32: one-CTA tiles and pairs in a slot
-// of the workspace per CTA, while the other accumulator fills; split tiles in
-// registers. 65536 x 2560 x 2560, both products: 1288 us without, 1296 every 512
-// steps, 1313 every 128, 1330 every 64.
+// (measured; where signs mix 1.6e-9 of the magnitudes and less): fp16's half step,
+// 2^-11, at 72,000 rows. dW's sums over rows are therefore taken out of the
+// accumulators every 256 steps (16384 rows, 1.1e-4) and added in FP32: one-CTA
+// tiles and pairs in a slot of the workspace per CTA, while the other accumulator
+// fills; split tiles in registers. 65536 x 2560 x 2560, both products: 1288 us
+// without, 1296 every 512 steps, 1311 every 256, 1313 every 128, 1330 every 64.
 constexpr int kDrain = 256;            // contraction steps
 constexpr int kSumFloats = 128 * 256;  // a CTA's accumulator
 

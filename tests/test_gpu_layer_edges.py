@@ -252,7 +252,7 @@ def test_long_sums_of_one_sign(R, off, n_in, n_out):
     E = len(off) - 1 if off else 1
     g = torch.Generator(device="cuda").manual_seed(R)
     x = (0.5 + torch.rand((R, n_in), generator=g, device="cuda", dtype=torch.float16))
-    dy = (0.5 + torch.rand((R, n_out), generator=g, device="cuda", dtype=torch.float16)) * 2.0 ** -10
+    dy = (0.5 + torch.rand((R, n_out), generator=g, device="cuda", dtype=torch.float16)) / 1024
     cfg = bm.linear_cfg(n_in, n_out, E, dtype="fp16")
     ws = torch.empty(bm.beam_moe_linear_workspace_size(cfg, R, True), dtype=torch.uint8,
                      device="cuda")
